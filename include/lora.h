@@ -78,7 +78,8 @@ typedef enum {
   LORA_ERR_TIMEOUT = 7,            /* a kernel gave up on a bounded wait */
   LORA_ERR_UNSUPPORTED_DEVICE = 8, /* current device is not sm_100 */
   LORA_ERR_ALIAS = 9,              /* an output overlaps an input */
-  LORA_ERR_FLAGS = 10              /* a flags argument has an unknown bit set */
+  LORA_ERR_FLAGS = 10,             /* a flags argument has an unknown bit set */
+  LORA_ERR_DROPOUT = 11            /* p outside [0, 1), or p > 0 without a seed and offset */
 } lora_status_t;
 
 /* ABI version of the loaded library (LORA_ABI_VERSION it was built with). */
@@ -337,6 +338,76 @@ lora_status_t lora_merge_batched_scaled(const lora_merge_desc_t* descs, int32_t 
  * copy is only read).
  */
 lora_status_t lora_restore(const void* W_src, void* W_dst, int64_t n_elems, void* stream);
+
+/*
+ * Dropout on the adapter branch (LoRA's usual form: the base product sees X,
+ * the adapter a dropped X):
+ *     T  = s/(1-p) (m * X) A^T,   Y = X W^T + T B^T
+ *     dT = s dY B,  dB = dY^T T,  dA = dT^T (m * X)/(1-p),
+ *     dX = dY W + m * (dT A)/(1-p)
+ * The mask m is never stored.  It comes from a counter-based generator
+ * (Philox4x32 with 7 rounds): X's element (i, k) is kept when lane k % 8 of
+ * the 8 16-bit lanes (low half of word 0 first) of the block with counter
+ * (k / 8, i, offset low word, offset high word) and key (seed low, seed
+ * high) is at least t = round(65536 p); 1-p stands for 1 - t/65536.  A
+ * dropped value counts as zero even if it is infinite or NaN.
+ *   `rng`: DEVICE memory, 16-byte aligned, two uint64: seed and offset, read
+ *   when the kernels run.  A captured graph therefore draws a new mask at
+ *   each replay after which the caller changed them (an offset that grows
+ *   by one a step is enough), and the backward draws its forward's mask when
+ *   it is given the same two values.  p == 0 is no dropout (rng may be NULL).
+ * Scale, flags, fp32 gradients, M == 0 and repeatability are as in
+ * lora_bwd_scaled.  `workspace` is one of lora_bwd_workspace_size bytes for
+ * the forward too, which leaves T (here with s/(1-p), bf16) in it: with
+ * LORA_BWD_T_SAVED the backward takes it from there, else it is computed
+ * again.  It is not interchangeable with lora_fwd_save's.
+ */
+lora_status_t lora_fwd_dropout(const void* X, const void* W, const void* A, const void* B, void* Y,
+                               int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale,
+                               float p, const void* rng, void* workspace, size_t workspace_bytes, void* stream);
+lora_status_t lora_bwd_dropout(const void* X, const void* W, const void* A, const void* B,
+                               const void* dY, void* dX, void* dA, void* dB,
+                               int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale,
+                               float p, const void* rng, void* workspace, size_t workspace_bytes,
+                               uint32_t flags, void* stream);
+
+/*
+ * An 8-bit base weight: Wq[d_out, d_in] e4m3 codes and Ws[ceil(d_out/128),
+ * ceil(d_in/128)] e8m0 bytes, row-major, 16-byte aligned: the value of a
+ * code in a 128 x 128 block with byte b is code * 2^(b - 127).  2^(b - 127)
+ * is the smallest power of two, at least 2^-127, with which the block's
+ * largest magnitude is at most 448; a zero block has b = 127, and a block
+ * that holds an infinity or a NaN b = 255 (NaN).  The code is then the
+ * value's only rounding (nearest even).  Blocks with b of the caller's own
+ * choice are used in the same way.  d_in is a multiple of 16; lora_dequantize
+ * rounds each value to bf16, which is exact unless it is subnormal there.
+ */
+lora_status_t lora_quantize_fp8(const void* W, void* Wq, void* Ws, int64_t d_out, int64_t d_in, void* stream);
+lora_status_t lora_dequantize_fp8(const void* Wq, const void* Ws, void* W, int64_t d_out, int64_t d_in, void* stream);
+
+/*
+ * The layer over an 8-bit base, with or without dropout:
+ *     Y  = Xq Wq^T + T B^T            dX = dYq Wq + m * (dT A)/(1-p)
+ * T, dT, dA, dB as in lora_fwd_dropout (from X and dY themselves, in bf16).
+ * Xq and dYq are X and dY rounded to e4m3 within the call, with one
+ * power-of-two scale for each row and each 128 consecutive values of the
+ * contraction, chosen as for the weight; Wq stands for its values.  Products
+ * are exact, sums fp32, one rounding to bf16.  The gradient passes the
+ * rounding of X as if it were not there.  d_in and d_out are multiples of
+ * 16.  A row's group that holds an infinity or a NaN makes the row's outputs
+ * NaN.  `workspace`: lora_fp8_workspace_size bytes, for forward and backward;
+ * with LORA_BWD_T_SAVED the backward takes T from the forward's.  The
+ * forward rounds X for itself, from a single token up.
+ */
+size_t lora_fp8_workspace_size(int64_t M, int64_t d_in, int64_t d_out, int32_t r);
+lora_status_t lora_fwd_fp8(const void* X, const void* Wq, const void* Ws, const void* A, const void* B, void* Y,
+                           int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale,
+                           float p, const void* rng, void* workspace, size_t workspace_bytes, void* stream);
+lora_status_t lora_bwd_fp8(const void* X, const void* Wq, const void* Ws, const void* A, const void* B,
+                           const void* dY, void* dX, void* dA, void* dB,
+                           int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale,
+                           float p, const void* rng, void* workspace, size_t workspace_bytes,
+                           uint32_t flags, void* stream);
 
 /*
  * Synchronizes the current device, returns LORA_ERR_TIMEOUT if any kernel

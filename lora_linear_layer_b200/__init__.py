@@ -22,6 +22,7 @@ STATUS = {
     0: "LORA_OK", 1: "LORA_ERR_NULL", 2: "LORA_ERR_SHAPE", 3: "LORA_ERR_ALIGN",
     4: "LORA_ERR_RANK", 5: "LORA_ERR_WORKSPACE", 6: "LORA_ERR_CUDA",
     7: "LORA_ERR_TIMEOUT", 8: "LORA_ERR_UNSUPPORTED_DEVICE", 9: "LORA_ERR_ALIAS", 10: "LORA_ERR_FLAGS",
+    11: "LORA_ERR_DROPOUT",
 }
 LORA_BWD_FP32_GRADS = 1
 LORA_BWD_T_SAVED = 2
@@ -121,6 +122,22 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = ctypes.c_int
             fn.argtypes = list(getattr(L, base).argtypes)
+        u32 = ctypes.c_uint32
+        tail = [i64, i64, i64, i32, f32, f32, vp, vp, sz]  # sizes, scale, p, rng, workspace
+        L.lora_fwd_dropout.restype = ctypes.c_int
+        L.lora_fwd_dropout.argtypes = [vp] * 5 + tail + [vp]
+        L.lora_bwd_dropout.restype = ctypes.c_int
+        L.lora_bwd_dropout.argtypes = [vp] * 8 + tail + [u32, vp]
+        L.lora_fwd_fp8.restype = ctypes.c_int
+        L.lora_fwd_fp8.argtypes = [vp] * 6 + tail + [vp]
+        L.lora_bwd_fp8.restype = ctypes.c_int
+        L.lora_bwd_fp8.argtypes = [vp] * 9 + tail + [u32, vp]
+        L.lora_fp8_workspace_size.restype = sz
+        L.lora_fp8_workspace_size.argtypes = [i64, i64, i64, i32]
+        for name in ("lora_quantize_fp8", "lora_dequantize_fp8"):
+            fn = getattr(L, name)
+            fn.restype = ctypes.c_int
+            fn.argtypes = [vp, vp, vp, i64, i64, vp]
         _lib_handle = L
         return L
 
@@ -446,6 +463,159 @@ def lora_restore(W_src, W_dst, stream=None) -> None:
     _check_tensor(W_dst, "W_dst", tuple(W_src.shape))
     code = lib().lora_restore(_ptr(W_src), _ptr(W_dst), W_src.numel(), _stream(stream))
     _raise(code, "lora_restore")
+
+
+# ------------------------------------- dropout and the 8-bit base ----
+
+def _check_typed(t, name: str, dtype, shape: Tuple[int, ...], device):
+    torch = _tm()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _workspace_arg(workspace, device):
+    torch = _tm()
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _rng_arg(rng, device):
+    if rng is None:
+        return None
+    _check_typed(rng, "rng", _tm().int64, (2,), device)
+    return _ptr(rng)
+
+
+def _scales_shape(d_out: int, d_in: int) -> Tuple[int, int]:
+    return (d_out + 127) // 128, (d_in + 127) // 128
+
+
+def _on_device(device, stream, call):
+    """call(stream handle) with `device` current (the library launches on the
+    current device)."""
+    torch = _tm()
+    if device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _layer_args(X, W, Ws, A, B, rng, workspace, outs, grads=()):
+    """Checks the tensors of a layer call, all on X's device; returns their
+    pointers, the sizes and the rng and workspace arguments."""
+    torch = _tm()
+    bf16 = torch.bfloat16
+    if not isinstance(X, torch.Tensor) or not isinstance(B, torch.Tensor):
+        raise TypeError("X and B must be torch.Tensors")
+    if X.dim() != 2 or B.dim() != 2:
+        raise ValueError(f"X and B must be 2-D, got {X.dim()}-D and {B.dim()}-D")
+    M, d_in = X.shape
+    d_out, r = B.shape
+    dev = X.device
+    shapes = {"X": (M, d_in), "A": (r, d_in), "B": (d_out, r), "Y": (M, d_out), "dY": (M, d_out), "dX": (M, d_in),
+              "dA": (r, d_in), "dB": (d_out, r)}
+    _check_typed(X, "X", bf16, shapes["X"], dev)
+    ptrs = [_ptr(X)]
+    if Ws is None:
+        _check_typed(W, "W", bf16, (d_out, d_in), dev)
+        ptrs.append(_ptr(W))
+    else:
+        _check_typed(W, "Wq", torch.float8_e4m3fn, (d_out, d_in), dev)
+        _check_typed(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), dev)
+        ptrs += [_ptr(W), _ptr(Ws)]
+    for name, t, dtype in (("A", A, bf16), ("B", B, bf16)) + tuple(outs) + tuple(grads):
+        _check_typed(t, name, dtype, shapes[name], dev)
+        ptrs.append(_ptr(t))
+    return ptrs, (M, d_in, d_out, r), _rng_arg(rng, dev), _workspace_arg(workspace, dev)
+
+
+def _adapter_fwd(name, X, W, Ws, A, B, Y, scale, p, rng, workspace, stream):
+    ptrs, sizes, rng_ptr, ws = _layer_args(X, W, Ws, A, B, rng, workspace, (("Y", Y, _tm().bfloat16),))
+    fn = getattr(lib(), name)
+    _raise(_on_device(X.device, stream, lambda st: fn(*ptrs, *sizes, float(scale), float(p), rng_ptr, *ws, st)), name)
+
+
+def _adapter_bwd(name, X, W, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream):
+    torch = _tm()
+    gdt = torch.float32 if int(flags) & LORA_BWD_FP32_GRADS else torch.bfloat16
+    ptrs, sizes, rng_ptr, ws = _layer_args(
+        X, W, Ws, A, B, rng, workspace, (("dY", dY, torch.bfloat16), ("dX", dX, torch.bfloat16)),
+        (("dA", dA, gdt), ("dB", dB, gdt)))
+    fn = getattr(lib(), name)
+    _raise(_on_device(X.device, stream,
+                      lambda st: fn(*ptrs, *sizes, float(scale), float(p), rng_ptr, *ws, int(flags), st)), name)
+
+
+def lora_fwd_dropout(X, W, A, B, Y, scale: float, p: float, rng, workspace, stream=None) -> None:
+    """Y = X W^T + T B^T with T = scale/(1-p) (m * X) A^T, the mask m drawn
+    from ``rng``, an int64 CUDA tensor [seed, offset] (see include/lora.h).
+    ``workspace`` (lora_bwd_workspace_size bytes) receives T."""
+    _adapter_fwd("lora_fwd_dropout", X, W, None, A, B, Y, scale, p, rng, workspace, stream)
+
+
+def lora_bwd_dropout(X, W, A, B, dY, dX, dA, dB, scale: float, p: float, rng, workspace, flags: int = 0,
+                     stream=None) -> None:
+    """The backward of lora_fwd_dropout for the same ``rng`` values; with
+    LORA_BWD_T_SAVED the workspace is the one the forward left T in."""
+    _adapter_bwd("lora_bwd_dropout", X, W, None, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
+
+
+def lora_fp8_workspace_size(M: int, d_in: int, d_out: int, r: int) -> int:
+    return int(lib().lora_fp8_workspace_size(int(M), int(d_in), int(d_out), int(r)))
+
+
+def lora_fwd_fp8(X, Wq, Ws, A, B, Y, scale: float, workspace, p: float = 0.0, rng=None, stream=None) -> None:
+    """Y = Xq Wq^T + T B^T over an 8-bit base: Wq float8_e4m3fn [d_out, d_in],
+    Ws float8_e8m0fnu [ceil(d_out/128), ceil(d_in/128)] (see include/lora.h);
+    ``workspace`` of lora_fp8_workspace_size bytes."""
+    _adapter_fwd("lora_fwd_fp8", X, Wq, Ws, A, B, Y, scale, p, rng, workspace, stream)
+
+
+def lora_bwd_fp8(X, Wq, Ws, A, B, dY, dX, dA, dB, scale: float, workspace, p: float = 0.0, rng=None, flags: int = 0,
+                 stream=None) -> None:
+    """The backward of lora_fwd_fp8: dX through Wq, dA and dB of the adapter."""
+    _adapter_bwd("lora_bwd_fp8", X, Wq, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
+
+
+def _quant_args(W, Wq, Ws):
+    torch = _tm()
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be a 2-D tensor")
+    d_out, d_in = W.shape
+    _check_typed(W, "W", torch.bfloat16, (d_out, d_in), W.device)
+    _check_typed(Wq, "Wq", torch.float8_e4m3fn, (d_out, d_in), W.device)
+    _check_typed(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), W.device)
+    return d_out, d_in
+
+
+def lora_quantize_fp8(W, Wq, Ws, stream=None) -> None:
+    """W (bf16) -> Wq (e4m3 codes) and Ws (one power of two for each
+    128 x 128 block; see include/lora.h)."""
+    d_out, d_in = _quant_args(W, Wq, Ws)
+    fn = lib().lora_quantize_fp8
+    _raise(_on_device(W.device, stream, lambda st: fn(_ptr(W), _ptr(Wq), _ptr(Ws), d_out, d_in, st)),
+           "lora_quantize_fp8")
+
+
+def lora_dequantize_fp8(Wq, Ws, W, stream=None) -> None:
+    """Wq, Ws -> the bf16 values they stand for."""
+    d_out, d_in = _quant_args(W, Wq, Ws)
+    fn = lib().lora_dequantize_fp8
+    _raise(_on_device(W.device, stream, lambda st: fn(_ptr(Wq), _ptr(Ws), _ptr(W), d_out, d_in, st)),
+           "lora_dequantize_fp8")
 
 
 def lora_get_device_status() -> int:

@@ -1,0 +1,503 @@
+// adapter_api.cuh - entry points of the adapter with dropout and of the
+// 8-bit base: argument rules, launch configuration, launches.
+// Part of the single translation unit built from lora_api.cu.
+#pragma once
+
+#include "adapter_pass.cuh"
+#include "lowrank_gemm.cuh"
+
+namespace {
+
+// ------------------------------------------------------------- arguments ----
+
+// p and rng -> the mask's arguments.  p == 0 is no dropout (rng is ignored).
+lora_status_t drop_args(float p, const void* rng, DropArgs& d) {
+  d = DropArgs{nullptr, 0u, 1.0f};
+  if (!(p >= 0.0f) || p >= 1.0f) return LORA_ERR_DROPOUT;
+  const int thr = int(double(p) * 65536.0 + 0.5);
+  if (thr > 65535) return LORA_ERR_DROPOUT;
+  if (p == 0.0f) return LORA_OK;
+  if (rng == nullptr) return LORA_ERR_DROPOUT;
+  if (!aligned16(rng)) return LORA_ERR_ALIGN;
+  d.rng = reinterpret_cast<const uint64_t*>(rng);
+  d.thr = uint32_t(thr);
+  d.inv_keep = float(65536.0 / double(65536 - thr));
+  return LORA_OK;
+}
+
+int64_t qblocks(int64_t n) { return (n + kQBlock - 1) / kQBlock; }
+
+lora_status_t check_sizes_fp8(int64_t M, int64_t d_in, int64_t d_out, int32_t r) {
+  const lora_status_t s = check_sizes(M, d_in, d_out, r);
+  if (s != LORA_OK) return s;
+  return (d_in % 16) != 0 || (d_out % 16) != 0 ? LORA_ERR_SHAPE : LORA_OK;
+}
+
+// The 8-bit layer's workspace: T and dT as the backward's, then the codes of
+// X or dY and their scales.
+struct Fp8Workspace {
+  size_t off_codes, off_scales, total;
+};
+
+Fp8Workspace fp8_workspace(int64_t M, int64_t d_in, int64_t d_out, int32_t r) {
+  const size_t wide = size_t(std::max(d_in, d_out));
+  Fp8Workspace w;
+  w.off_codes = bwd_workspace(M, r).total;
+  w.off_scales = w.off_codes + align256(size_t(M) * wide);
+  w.total = w.off_scales + align256(size_t(M) * ((wide + 511) / 512) * 4);
+  return w;
+}
+
+// Base weight of a call: bf16 (scales NULL) or e4m3 codes with block scales.
+struct Base {
+  const void* w;
+  const void* scales;
+  bool fp8() const { return scales != nullptr; }
+};
+
+// -------------------------------------------------------- adapter passes ----
+
+struct PassCfg {
+  int RCW;
+  uint32_t smem;
+  PassArgs args;
+};
+
+// Three stages (36 KB each for K-major P at r = 16: two blocks per SM); the
+// splits of a row tile form one cluster, as many as fill the resident block
+// slots, at most 8 and at least 256 values of the contraction each.
+void pick_pass(int64_t rows, int64_t K, int r, bool p_mn, bool r_mn, int out_mode, int64_t launch_tiles, int sm_count,
+               PassCfg& c) {
+  const int r_pad = r_pad_of(r);
+  c.RCW = rcw_of(r_pad);
+  PassArgs& a = c.args;
+  std::memset(&a, 0, sizeof(a));
+  a.n_rchunks = (r_pad + c.RCW - 1) / c.RCW;
+  a.stages = 3;
+  c.smem = PassLayout(p_mn, r_mn, c.RCW, r_pad, a.n_rchunks, a.stages).total + 1024;
+  const int per_sm = std::max(1, std::min<int>(int(kSmemPerSM / (c.smem + 1024)), 2048 / kPassThreads));
+  const int block_k = p_mn ? 64 : 128;
+  const int nb = int((K + block_k - 1) / block_k);
+  const int tiles = int(std::max<int64_t>(1, launch_tiles));
+  int splits = std::max(1, std::min({per_sm * sm_count / tiles, 8, std::max(1, nb * block_k / 256)}));
+  a.nb_per_split = std::max(1, (nb + splits - 1) / splits);
+  splits = std::max(1, (nb + a.nb_per_split - 1) / a.nb_per_split);
+  a.rows = int32_t(rows);
+  a.K = int32_t(K);
+  a.r_pad = r_pad;
+  a.r = r;
+  a.splits = splits;
+  a.out_mode = out_mode;
+  a.r_mn = r_mn ? 1 : 0;
+  a.scale = 1.0f;
+  a.drop = DropArgs{nullptr, 0u, 1.0f};
+  a.wait_limit_ns = kWaitLimitNs;
+}
+
+// Two jobs of one launch share its split count.
+void resplit_pass(PassCfg& c, int splits, bool p_mn) {
+  const int block_k = p_mn ? 64 : 128;
+  const int nb = int((int64_t(c.args.K) + block_k - 1) / block_k);
+  c.args.splits = splits;
+  c.args.nb_per_split = std::max(1, (nb + splits - 1) / splits);
+}
+
+struct PassMaps {
+  CUtensorMap p, r;
+};
+
+template <bool P_MN, int RCW, bool QUANT>
+lora_status_t launch_pass_t(const PassMaps& m0, const PassCfg& c0, const PassMaps* m1, const PassCfg* c1,
+                            cudaStream_t st) {
+  auto kern = adapter_pass_kernel<P_MN, RCW, QUANT>;
+  const uint32_t smem = c1 != nullptr ? std::max(c0.smem, c1->smem) : c0.smem;
+  if (!ensure_smem_attr(kern, smem)) return LORA_ERR_CUDA;
+  const int t0 = int((int64_t(c0.args.rows) + 127) / 128);
+  const int t1 = c1 != nullptr ? int((int64_t(c1->args.rows) + 127) / 128) : 0;
+  const dim3 cl(1, unsigned(c0.args.splits), 1);
+  const PassMaps& second = m1 != nullptr ? *m1 : m0;
+  return launch_ex("adapter pass", kern, dim3(unsigned(t0 + t1), unsigned(c0.args.splits)), dim3(kPassThreads), smem,
+                   st, &cl, m0.p, m0.r, second.p, second.r, c0.args, c1 != nullptr ? c1->args : c0.args, int32_t(t0));
+}
+
+template <bool P_MN, bool QUANT>
+lora_status_t launch_pass(const PassMaps& m0, const PassCfg& c0, cudaStream_t st, const PassMaps* m1 = nullptr,
+                          const PassCfg* c1 = nullptr) {
+  if (c0.RCW == 16) return launch_pass_t<P_MN, 16, QUANT>(m0, c0, m1, c1, st);
+  if (c0.RCW == 32) return launch_pass_t<P_MN, 32, QUANT>(m0, c0, m1, c1, st);
+  return launch_pass_t<P_MN, 64, QUANT>(m0, c0, m1, c1, st);
+}
+
+// T = scale (m * X) A^T into `Tws`; with `codes`, X's codes and scales too.
+lora_status_t launch_down(const void* X, const void* A, int64_t M, int64_t d_in, int32_t r, float scale,
+                          const DropArgs& drop, __nv_bfloat16* Tws, uint8_t* codes, uint8_t* scales, int sm_count,
+                          cudaStream_t st) {
+  PassCfg c;
+  pick_pass(M, d_in, r, false, false, OUT_ROWS_RPAD, (M + 127) / 128, sm_count, c);
+  c.args.out = Tws;
+  c.args.scale = scale * drop.inv_keep;
+  c.args.drop = drop;
+  c.args.codes = codes;
+  c.args.scales = scales;
+  PassMaps m;
+  if (!make_map(&m.p, X, d_in, M, d_in, 64, 128, 128) ||
+      !make_map(&m.r, A, d_in, r, d_in, 64, uint32_t(c.args.r_pad), 128))
+    return LORA_ERR_CUDA;
+  return codes != nullptr ? launch_pass<false, true>(m, c, st) : launch_pass<false, false>(m, c, st);
+}
+
+// -------------------------------------------------------- low-rank GEMMs ----
+
+struct LrCfg {
+  int BN;
+  uint32_t smem;
+  LrArgs args;
+};
+
+uint32_t lr_stage_bytes(bool fp8, bool mn, int BN) {
+  if (fp8) {
+    return mn ? (BN == 224 ? LrShape<true, true, 224>::kStage : LrShape<true, true, 128>::kStage)
+              : (BN == 224 ? LrShape<true, false, 224>::kStage : LrShape<true, false, 128>::kStage);
+  }
+  return mn ? (BN == 256 ? LrShape<false, true, 256>::kStage : LrShape<false, true, 128>::kStage)
+            : (BN == 256 ? LrShape<false, false, 256>::kStage : LrShape<false, false, 128>::kStage);
+}
+
+// OUT[M, N] over the contraction K: the wide tile (224 columns for 8 bits,
+// 256 for bf16) unless 128-wide ones, each with its share of fixed cost (32
+// columns' worth), finish sooner.
+void pick_lr(int64_t M, int64_t N, int64_t K, int r, bool fp8, bool mn, int sm_count, LrCfg& c) {
+  const int64_t clusters = sm_count / 2;
+  const int64_t num_m = (M + 255) / 256;
+  auto cost = [&](int bn) {
+    const int64_t tiles = num_m * ((N + bn - 1) / bn);
+    return ((tiles + clusters - 1) / clusters) * int64_t(bn + 32);
+  };
+  const int wide = fp8 ? 224 : 256;
+  c.BN = cost(128) < cost(wide) ? 128 : wide;
+  const uint32_t stage = lr_stage_bytes(fp8, mn, c.BN);
+  auto stages_for = [&](int ep_bufs) {
+    return std::min(8, int((kSmemMax - LrLayout(stage, fp8, 0, ep_bufs).total - 1024) / stage));
+  };
+  std::memset(&c.args, 0, sizeof(c.args));
+  FusedArgs& a = c.args.f;
+  a.stages = stages_for(1);
+  a.ep_bufs = stages_for(2) >= a.stages ? 2 : 1;
+  c.smem = LrLayout(stage, fp8, a.stages, a.ep_bufs).total + 1024;
+  a.M = int32_t(M);
+  a.N = int32_t(N);
+  a.K = int32_t(K);
+  a.r_pad = r_pad_of(r);
+  a.scale = 1.0f;
+  a.num_m = int32_t(num_m);
+  a.num_n = int32_t((N + c.BN - 1) / c.BN);
+  a.band_w = a.num_n;  // single-tile runs dealt round-robin use no bands
+  a.n_bands = 1;
+  a.run_l = 1;
+  a.wait_limit_ns = kWaitLimitNs;
+  c.args.drop = DropArgs{nullptr, 0u, 1.0f};
+}
+
+template <bool FP8, bool MN, bool DROP, int BN>
+lora_status_t launch_lr_t(const CUtensorMap* maps, const LrCfg& c, int sm_count, cudaStream_t st) {
+  auto kern = lowrank_gemm_kernel<FP8, MN, DROP, BN>;
+  if (!ensure_smem_attr(kern, c.smem)) return LORA_ERR_CUDA;
+  const int64_t tiles = int64_t(c.args.f.num_m) * c.args.f.num_n;
+  const int clusters = int(std::min<int64_t>(tiles, max_clusters(kern, 2, c.smem, sm_count)));
+  const dim3 cl(2, 1, 1);
+  return launch_ex("low-rank GEMM", kern, dim3(unsigned(clusters * 2)), dim3(LrShape<FP8, MN, BN>::kThreads), c.smem,
+                   st, &cl, maps[0], maps[1], maps[2], maps[3], maps[4], c.args);
+}
+
+template <bool MN, bool DROP>
+lora_status_t launch_lr(bool fp8, const CUtensorMap* maps, const LrCfg& c, int sm_count, cudaStream_t st) {
+  if (fp8)
+    return c.BN == 224 ? launch_lr_t<true, MN, DROP, 224>(maps, c, sm_count, st)
+                       : launch_lr_t<true, MN, DROP, 128>(maps, c, sm_count, st);
+  return c.BN == 256 ? launch_lr_t<false, MN, DROP, 256>(maps, c, sm_count, st)
+                     : launch_lr_t<false, MN, DROP, 128>(maps, c, sm_count, st);
+}
+
+// Y = X W^T + T B^T from T (bf16 [M, r_pad], scale included); for an 8-bit
+// base X is its codes, with `x_scales`.
+lora_status_t launch_up(const void* X, const uint8_t* x_scales, const Base& W, const void* B, void* Y,
+                        const __nv_bfloat16* Tws, int64_t M, int64_t d_in, int64_t d_out, int32_t r, int sm_count,
+                        cudaStream_t st) {
+  LrCfg c;
+  const bool fp8 = W.fp8();
+  pick_lr(M, d_out, d_in, r, fp8, false, sm_count, c);
+  c.args.f.out = reinterpret_cast<__nv_bfloat16*>(Y);
+  const uint32_t bnc = uint32_t(c.BN / 2);
+  const uint64_t r_pad = uint64_t(r_pad_of(r));
+  CUtensorMap maps[5];
+  const bool ok = fp8 ? make_map_u8(&maps[0], X, d_in, M, d_in, 128, 128) &&
+                            make_map_u8(&maps[1], W.w, d_in, d_out, d_in, 128, bnc)
+                      : make_map(&maps[0], X, d_in, M, d_in, 64, 128, 128) &&
+                            make_map(&maps[1], W.w, d_in, d_out, d_in, 64, bnc, 128);
+  if (!ok || !make_map(&maps[2], Tws, r_pad, M, r_pad, 64, 128, 128) ||
+      !make_map(&maps[3], B, r, d_out, r, 64, bnc, 128) ||
+      !make_map(&maps[4], Y, d_out, M, d_out, kEpCols, 32, kEpCols * 2))
+    return LORA_ERR_CUDA;
+  if (fp8) {
+    c.args.p_scales = reinterpret_cast<const uint32_t*>(x_scales);
+    c.args.q_scales = reinterpret_cast<const uint8_t*>(W.scales);
+    c.args.qs_n = int32_t(qblocks(d_out));
+    c.args.qs_k = int32_t(qblocks(d_in));
+    c.args.qs_ld_n = c.args.qs_k;
+    c.args.qs_ld_k = 1;
+  }
+  return launch_lr<false, false>(fp8, maps, c, sm_count, st);
+}
+
+// dX = dY W + m * (dT A)/(1-p).
+lora_status_t launch_dx(const void* dY, const uint8_t* dy_scales, const Base& W, const void* A, void* dX,
+                        const __nv_bfloat16* dTws, int64_t M, int64_t d_in, int64_t d_out, int32_t r,
+                        const DropArgs& drop, int sm_count, cudaStream_t st) {
+  LrCfg c;
+  const bool fp8 = W.fp8();
+  pick_lr(M, d_in, d_out, r, fp8, true, sm_count, c);
+  c.args.f.out = reinterpret_cast<__nv_bfloat16*>(dX);
+  c.args.drop = drop;
+  const uint64_t r_pad = uint64_t(r_pad_of(r));
+  CUtensorMap maps[5];
+  const bool ok = fp8 ? make_map_u8(&maps[0], dY, d_out, M, d_out, 128, 128) &&
+                            make_map_u8(&maps[1], W.w, d_in, d_out, d_in, 128, 128)
+                      : make_map(&maps[0], dY, d_out, M, d_out, 64, 128, 128) &&
+                            make_map(&maps[1], W.w, d_in, d_out, d_in, 64, 64, 128);
+  if (!ok || !make_map(&maps[2], dTws, r_pad, M, r_pad, 64, 128, 128) ||
+      !make_map(&maps[3], A, d_in, r, d_in, 64, 64, 128) ||
+      !make_map(&maps[4], dX, d_in, M, d_in, kEpCols, 32, kEpCols * 2))
+    return LORA_ERR_CUDA;
+  if (fp8) {
+    c.args.p_scales = reinterpret_cast<const uint32_t*>(dy_scales);
+    c.args.q_scales = reinterpret_cast<const uint8_t*>(W.scales);
+    c.args.qs_n = int32_t(qblocks(d_in));
+    c.args.qs_k = int32_t(qblocks(d_out));
+    c.args.qs_ld_n = 1;
+    c.args.qs_ld_k = c.args.qs_n;
+  }
+  return drop.rng != nullptr ? launch_lr<true, true>(fp8, maps, c, sm_count, st)
+                             : launch_lr<true, false>(fp8, maps, c, sm_count, st);
+}
+
+// --------------------------------------------------------- whole layers ----
+
+// Forward.  Arguments already validated.
+lora_status_t adapter_fwd_run(const void* X, const Base& W, const void* A, const void* B, void* Y, int64_t M,
+                              int64_t d_in, int64_t d_out, int32_t r, float scale, const DropArgs& drop,
+                              void* workspace, cudaStream_t st) {
+  DeviceInfo dev;
+  lora_status_t s = device_info(dev);
+  if (s != LORA_OK || M == 0) return s;
+  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
+  __nv_bfloat16* const Tws = reinterpret_cast<__nv_bfloat16*>(ws + bwd_workspace(M, r).off_t);
+  const Fp8Workspace q = fp8_workspace(M, d_in, d_out, r);
+  uint8_t* const codes = W.fp8() ? ws + q.off_codes : nullptr;
+  uint8_t* const scales = W.fp8() ? ws + q.off_scales : nullptr;
+  if ((s = launch_down(X, A, M, d_in, r, scale, drop, Tws, codes, scales, dev.sm_count, st)) != LORA_OK) return s;
+  return launch_up(W.fp8() ? codes : X, scales, W, B, Y, Tws, M, d_in, d_out, r, dev.sm_count, st);
+}
+
+// Backward.  Arguments already validated.
+//  1. dT = s dY B (with an 8-bit base also dY's codes), and T unless saved;
+//  2. dB = dY^T T and dA = dT^T (m * X)/(1-p), one launch;
+//  3. dX.
+lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const void* B, const void* dY, void* dX,
+                              void* dA, void* dB, int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale,
+                              const DropArgs& drop, void* workspace, uint32_t flags, cudaStream_t st) {
+  const bool f32 = (flags & LORA_BWD_FP32_GRADS) != 0u;
+  const bool saved = (flags & LORA_BWD_T_SAVED) != 0u;
+  const bool fp8 = W.fp8();
+  DeviceInfo dev;
+  lora_status_t s = device_info(dev);
+  if (s != LORA_OK) return s;
+  if (M == 0) {
+    const size_t gb = f32 ? 4 : 2;
+    if ((s = zero_bytes(dA, size_t(r) * size_t(d_in) * gb, st)) != LORA_OK) return s;
+    return zero_bytes(dB, size_t(d_out) * size_t(r) * gb, st);
+  }
+  const int sms = dev.sm_count;
+  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
+  const BwdWorkspace w = bwd_workspace(M, r);
+  const Fp8Workspace q = fp8_workspace(M, d_in, d_out, r);
+  __nv_bfloat16* const Tws = reinterpret_cast<__nv_bfloat16*>(ws + w.off_t);
+  __nv_bfloat16* const dTws = reinterpret_cast<__nv_bfloat16*>(ws + w.off_dt);
+  uint8_t* const codes = fp8 ? ws + q.off_codes : nullptr;
+  uint8_t* const scales = fp8 ? ws + q.off_scales : nullptr;
+  const int r_pad = r_pad_of(r);
+  const int rcw = rcw_of(r_pad);
+
+  if (!saved &&
+      (s = launch_down(X, A, M, d_in, r, scale, drop, Tws, nullptr, nullptr, sms, st)) != LORA_OK)
+    return s;
+  {
+    PassCfg c;
+    pick_pass(M, d_out, r, false, true, OUT_ROWS_RPAD, (M + 127) / 128, sms, c);
+    c.args.out = dTws;
+    c.args.scale = scale;
+    c.args.codes = codes;
+    c.args.scales = scales;
+    PassMaps m;
+    if (!make_map(&m.p, dY, d_out, M, d_out, 64, 128, 128) || !make_map(&m.r, B, r, d_out, r, rcw, 64, rcw * 2))
+      return LORA_ERR_CUDA;
+    s = fp8 ? launch_pass<false, true>(m, c, st) : launch_pass<false, false>(m, c, st);
+    if (s != LORA_OK) return s;
+  }
+  {
+    PassCfg cb, ca;
+    const int64_t tiles = (d_out + 127) / 128 + (d_in + 127) / 128;
+    pick_pass(d_out, M, r, true, true, OUT_ROWS_R, tiles, sms, cb);
+    pick_pass(d_in, M, r, true, true, OUT_COLS_R, tiles, sms, ca);
+    resplit_pass(ca, cb.args.splits, true);
+    cb.args.out = reinterpret_cast<__nv_bfloat16*>(dB);
+    cb.args.out_f32 = f32 ? 1 : 0;
+    ca.args.out = reinterpret_cast<__nv_bfloat16*>(dA);
+    ca.args.out_f32 = f32 ? 1 : 0;
+    ca.args.scale = drop.inv_keep;
+    ca.args.drop = drop;
+    PassMaps mb, ma;
+    if (!make_map(&mb.p, dY, d_out, M, d_out, 64, 64, 128) ||
+        !make_map(&mb.r, Tws, r_pad, M, r_pad, rcw, 64, rcw * 2) ||
+        !make_map(&ma.p, X, d_in, M, d_in, 64, 64, 128) ||
+        !make_map(&ma.r, dTws, r_pad, M, r_pad, rcw, 64, rcw * 2))
+      return LORA_ERR_CUDA;
+    if ((s = launch_pass<true, false>(mb, cb, st, &ma, &ca)) != LORA_OK) return s;
+  }
+  return launch_dx(fp8 ? codes : dY, scales, W, A, dX, dTws, M, d_in, d_out, r, drop, sms, st);
+}
+
+// Pointer and workspace rules of the four layer entry points (sizes already
+// checked); `grads`: dY, dX, dA, dB or NULL for a forward.
+lora_status_t check_adapter(const void* X, const Base& W, const void* A, const void* B, void* Y, const void* dY,
+                            void* dX, void* dA, void* dB, const DropArgs& drop, int64_t M, int64_t d_in,
+                            int64_t d_out, int32_t r, int gb, void* workspace, size_t workspace_bytes, bool fwd) {
+  const bool fp8 = W.fp8(), rows = M > 0;
+  const uint64_t m = uint64_t(M), k = uint64_t(d_in), n = uint64_t(d_out), rr = uint64_t(r);
+  const size_t need = !rows ? 0 : fp8 ? fp8_workspace(M, d_in, d_out, r).total : bwd_workspace(M, r).total;
+  const BufSpec in[7] = {{X, m * k * 2, rows},
+                         {W.w, k * n * (fp8 ? 1 : 2), true},
+                         {A, rr * k * 2, true},
+                         {B, n * rr * 2, true},
+                         {dY, m * n * 2, rows && !fwd},
+                         {drop.rng, 16, false},
+                         {W.scales, uint64_t(qblocks(d_in)) * uint64_t(qblocks(d_out)), fp8}};
+  const BufSpec ws{rows ? workspace : nullptr, need, false};
+  const BufSpec out_f[2] = {{Y, m * n * 2, rows}, ws};
+  const BufSpec out_b[4] = {{dX, m * k * 2, rows}, {dA, rr * k * uint64_t(gb), true},
+                            {dB, n * rr * uint64_t(gb), true}, ws};
+  const lora_status_t s = fwd ? check_bufs(in, 7, out_f, 2) : check_bufs(in, 7, out_b, 4);
+  if (s != LORA_OK) return s;
+  return check_workspace(workspace, workspace_bytes, need);
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status_t lora_fwd_dropout(const void* X, const void* W, const void* A, const void* B, void* Y, int64_t M,
+                               int64_t d_in, int64_t d_out, int32_t r, float scale, float p, const void* rng,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  lora_status_t s = check_sizes(M, d_in, d_out, r);
+  DropArgs drop;
+  if (s != LORA_OK || (s = drop_args(p, rng, drop)) != LORA_OK) return s;
+  const Base base{W, nullptr};
+  if ((s = check_adapter(X, base, A, B, Y, nullptr, nullptr, nullptr, nullptr, drop, M, d_in, d_out, r, 2, workspace,
+                         workspace_bytes, true)) != LORA_OK)
+    return s;
+  return adapter_fwd_run(X, base, A, B, Y, M, d_in, d_out, r, scale, drop, workspace,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+lora_status_t lora_bwd_dropout(const void* X, const void* W, const void* A, const void* B, const void* dY, void* dX,
+                               void* dA, void* dB, int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale,
+                               float p, const void* rng, void* workspace, size_t workspace_bytes, uint32_t flags,
+                               void* stream) {
+  if ((flags & ~kBwdFlags) != 0u) return LORA_ERR_FLAGS;
+  lora_status_t s = check_sizes(M, d_in, d_out, r);
+  DropArgs drop;
+  if (s != LORA_OK || (s = drop_args(p, rng, drop)) != LORA_OK) return s;
+  const Base base{W, nullptr};
+  const int gb = (flags & LORA_BWD_FP32_GRADS) != 0u ? 4 : 2;
+  if ((s = check_adapter(X, base, A, B, nullptr, dY, dX, dA, dB, drop, M, d_in, d_out, r, gb, workspace,
+                         workspace_bytes, false)) != LORA_OK)
+    return s;
+  return adapter_bwd_run(X, base, A, B, dY, dX, dA, dB, M, d_in, d_out, r, scale, drop, workspace, flags,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t lora_fp8_workspace_size(int64_t M, int64_t d_in, int64_t d_out, int32_t r) {
+  if (check_sizes_fp8(M, d_in, d_out, r) != LORA_OK || M == 0) return 0;
+  return fp8_workspace(M, d_in, d_out, r).total;
+}
+
+lora_status_t lora_fwd_fp8(const void* X, const void* Wq, const void* Ws, const void* A, const void* B, void* Y,
+                           int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale, float p, const void* rng,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  lora_status_t s = check_sizes_fp8(M, d_in, d_out, r);
+  DropArgs drop;
+  if (s != LORA_OK || (s = drop_args(p, rng, drop)) != LORA_OK) return s;
+  if (Ws == nullptr) return LORA_ERR_NULL;
+  const Base base{Wq, Ws};
+  if ((s = check_adapter(X, base, A, B, Y, nullptr, nullptr, nullptr, nullptr, drop, M, d_in, d_out, r, 2, workspace,
+                         workspace_bytes, true)) != LORA_OK)
+    return s;
+  return adapter_fwd_run(X, base, A, B, Y, M, d_in, d_out, r, scale, drop, workspace,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+lora_status_t lora_bwd_fp8(const void* X, const void* Wq, const void* Ws, const void* A, const void* B,
+                           const void* dY, void* dX, void* dA, void* dB, int64_t M, int64_t d_in, int64_t d_out,
+                           int32_t r, float scale, float p, const void* rng, void* workspace, size_t workspace_bytes,
+                           uint32_t flags, void* stream) {
+  if ((flags & ~kBwdFlags) != 0u) return LORA_ERR_FLAGS;
+  lora_status_t s = check_sizes_fp8(M, d_in, d_out, r);
+  DropArgs drop;
+  if (s != LORA_OK || (s = drop_args(p, rng, drop)) != LORA_OK) return s;
+  if (Ws == nullptr) return LORA_ERR_NULL;
+  const Base base{Wq, Ws};
+  const int gb = (flags & LORA_BWD_FP32_GRADS) != 0u ? 4 : 2;
+  if ((s = check_adapter(X, base, A, B, nullptr, dY, dX, dA, dB, drop, M, d_in, d_out, r, gb, workspace,
+                         workspace_bytes, false)) != LORA_OK)
+    return s;
+  return adapter_bwd_run(X, base, A, B, dY, dX, dA, dB, M, d_in, d_out, r, scale, drop, workspace, flags,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Sizes and buffers of the two weight conversions.
+static lora_status_t check_quant(const void* src, uint64_t src_b, const void* scales_in, const void* dst,
+                                 uint64_t dst_b, const void* scales_out, int64_t d_out, int64_t d_in) {
+  if (d_in <= 0 || d_out <= 0 || (d_in % 16) != 0 || d_in > (int64_t(1) << 30) || d_out > (int64_t(1) << 30))
+    return LORA_ERR_SHAPE;
+  const uint64_t nb = uint64_t(qblocks(d_in)) * uint64_t(qblocks(d_out));
+  if (nb > 0x7FFFFFFFull) return LORA_ERR_SHAPE;
+  const uint64_t e = uint64_t(d_in) * uint64_t(d_out);
+  const BufSpec in[2] = {{src, e * src_b, true}, {scales_in, nb, scales_out == nullptr}};
+  const BufSpec out[2] = {{dst, e * dst_b, true}, {scales_out, nb, scales_in == nullptr}};
+  return check_bufs(in, 2, out, 2);
+}
+
+lora_status_t lora_quantize_fp8(const void* W, void* Wq, void* Ws, int64_t d_out, int64_t d_in, void* stream) {
+  if (Ws == nullptr) return LORA_ERR_NULL;
+  lora_status_t s = check_quant(W, 2, nullptr, Wq, 1, Ws, d_out, d_in);
+  DeviceInfo dev;
+  if (s != LORA_OK || (s = device_info(dev)) != LORA_OK) return s;
+  const int64_t cb = qblocks(d_in);
+  return launch_ex("quantize", quantize_block_kernel, dim3(unsigned(cb * qblocks(d_out))), dim3(kQuantThreads), 0,
+                   reinterpret_cast<cudaStream_t>(stream), nullptr, reinterpret_cast<const uint8_t*>(W),
+                   reinterpret_cast<uint8_t*>(Wq), reinterpret_cast<uint8_t*>(Ws), int32_t(d_out), int32_t(d_in),
+                   int32_t(cb));
+}
+
+lora_status_t lora_dequantize_fp8(const void* Wq, const void* Ws, void* W, int64_t d_out, int64_t d_in, void* stream) {
+  if (Ws == nullptr) return LORA_ERR_NULL;
+  lora_status_t s = check_quant(Wq, 1, Ws, W, 2, nullptr, d_out, d_in);
+  DeviceInfo dev;
+  if (s != LORA_OK || (s = device_info(dev)) != LORA_OK) return s;
+  const int64_t cb = qblocks(d_in);
+  return launch_ex("dequantize", dequantize_block_kernel, dim3(unsigned(cb * qblocks(d_out))), dim3(kQuantThreads), 0,
+                   reinterpret_cast<cudaStream_t>(stream), nullptr, reinterpret_cast<const uint8_t*>(Wq),
+                   reinterpret_cast<const uint8_t*>(Ws), reinterpret_cast<uint8_t*>(W), int32_t(d_out), int32_t(d_in),
+                   int32_t(cb));
+}
+
+}  // extern "C"

@@ -1,0 +1,169 @@
+// fp8.cuh - e4m3 with a power-of-two scale for each block of 128.
+//
+// A group of values (a 128 x 128 block of a weight; 128 consecutive values
+// of one row of an activation or gradient) is held as e4m3 codes q and one
+// e8m0 byte b:  value = q 2^(b - 127).  2^(b - 127) is the smallest power of
+// two, at least 2^-127, with which the largest magnitude of the group is at
+// most 448, the largest e4m3 value; an empty (all zero) group has b = 127.
+// The division by a power of two is exact, so a code is the value's only
+// rounding (nearest even), and tcgen05.mma applies such scales itself.
+// A group that holds an infinity or a NaN gets b = 255, e8m0's NaN: every
+// product it enters is NaN, as in the unquantised layer's affected rows.
+//
+// The two weight kernels move 3 bytes an element and do nothing else of
+// weight: memory bound.  One block of 256 threads takes one 128 x 128 block
+// in registers (each thread 4 rows of 16 consecutive values: 8 16-byte loads
+// in flight), so W is read once, between the maximum and the codes.
+#pragma once
+
+#include "common.cuh"
+
+namespace lora {
+
+constexpr int kQBlock = 128;
+
+// |x| of two packed bf16, as integers that order like the magnitudes
+// (infinities and NaN above every finite value).
+__device__ __forceinline__ uint32_t abs_bf16x2(uint32_t v) { return v & 0x7FFF7FFFu; }
+
+__device__ __forceinline__ uint32_t amax_bf16x8(uint32_t m, uint4 v) {
+  m = __vmaxu2(m, abs_bf16x2(v.x));
+  m = __vmaxu2(m, abs_bf16x2(v.y));
+  m = __vmaxu2(m, abs_bf16x2(v.z));
+  return __vmaxu2(m, abs_bf16x2(v.w));
+}
+
+// The e8m0 byte of a group whose largest magnitude has these bf16 bits.
+// amax = 1.f * 2^x fits under 448 * 2^e = 1.75 * 2^(e + 8) with e = x - 8
+// when its fraction is at most .75 (96 of 128), else with e = x - 7.  A
+// subnormal bf16 (x < -126) is below 448 * 2^-127 in any case.
+__device__ __forceinline__ uint32_t e8m0_of_amax(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F80u) return 255u;
+  if (amax_bits == 0u) return 127u;
+  const int biased = int(amax_bits >> 7);
+  const int b = biased - ((amax_bits & 0x7Fu) <= 96u ? 8 : 7);
+  return b > 0 ? uint32_t(b) : 0u;
+}
+
+// 2^-(b - 127), the factor that a value is multiplied by (exact: b is at
+// most 247; 1 for the NaN scale).
+__device__ __forceinline__ float e8m0_inverse(uint32_t b) {
+  return b == 255u ? 1.0f : __uint_as_float((254u - b) << 23);
+}
+
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return b == 255u ? __uint_as_float(0x7FC00000u) : b == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+}
+
+// Two fp32 -> packed e4m3x2 (nearest even; magnitudes are at most 448 here),
+// `lo` in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four bf16 (two words) times `f` -> four codes.
+__device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, float f) {
+  const uint32_t lo = pack_e4m3x2(bf16lo_to_f32(a) * f, bf16hi_to_f32(a) * f);
+  const uint32_t hi = pack_e4m3x2(bf16lo_to_f32(b) * f, bf16hi_to_f32(b) * f);
+  return lo | (hi << 16);
+}
+
+__device__ __forceinline__ uint4 quant16(uint4 a, uint4 b, float f) {
+  return make_uint4(quant4(a.x, a.y, f), quant4(a.z, a.w, f), quant4(b.x, b.y, f), quant4(b.z, b.w, f));
+}
+
+// Two e4m3 codes (low 16 bits) -> two fp32 (through fp16, which holds every
+// e4m3 value).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(v)));
+  float2 f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}\n"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+constexpr int kQuantThreads = 256;
+
+// W[rows, cols] bf16 -> Wq codes (same layout) and Ws[ceil(rows/128),
+// ceil(cols/128)] bytes.  cols is a multiple of 16.  Grid: one block for each
+// 128 x 128 block of W, columns fastest.
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_block_kernel(const uint8_t* __restrict__ W, uint8_t* __restrict__ Wq, uint8_t* __restrict__ Ws,
+                          int32_t rows, int32_t cols, int32_t col_blocks) {
+  __shared__ uint32_t warp_max[kQuantThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int cb = int(blockIdx.x) % col_blocks, rb = int(blockIdx.x) / col_blocks;
+  const int col = cb * kQBlock + int(threadIdx.x & 7u) * 16;
+  const int row0 = rb * kQBlock + int(threadIdx.x >> 3);
+  uint4 v[4][2];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 32 * i;
+    const bool in = row < rows && col < cols;
+    const uint4* src = reinterpret_cast<const uint4*>(W + (size_t(row) * size_t(cols) + size_t(col)) * 2);
+    v[i][0] = in ? __ldcs(src) : make_uint4(0, 0, 0, 0);
+    v[i][1] = in ? __ldcs(src + 1) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = amax_bf16x8(amax_bf16x8(m, v[i][0]), v[i][1]);
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, s));
+  if ((threadIdx.x & 31u) == 0u) warp_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQuantThreads / 32; ++i) m = __vmaxu2(m, warp_max[i]);
+  const uint32_t b = e8m0_of_amax(max(m & 0xFFFFu, m >> 16));
+  const float f = e8m0_inverse(b);
+  if (threadIdx.x == 0) Ws[blockIdx.x] = uint8_t(b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 32 * i;
+    if (row < rows && col < cols)
+      *reinterpret_cast<uint4*>(Wq + size_t(row) * size_t(cols) + size_t(col)) = quant16(v[i][0], v[i][1], f);
+  }
+}
+
+// Wq, Ws -> W (bf16): each value q 2^(b - 127) rounded once (it is exact
+// unless it is below bf16's normal range).
+__global__ void __launch_bounds__(kQuantThreads)
+    dequantize_block_kernel(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Ws, uint8_t* __restrict__ W,
+                            int32_t rows, int32_t cols, int32_t col_blocks) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int cb = int(blockIdx.x) % col_blocks, rb = int(blockIdx.x) / col_blocks;
+  const int col = cb * kQBlock + int(threadIdx.x & 7u) * 16;
+  const int row0 = rb * kQBlock + int(threadIdx.x >> 3);
+  if (col >= cols) return;
+  uint4 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 32 * i;
+    q[i] = row < rows ? __ldcs(reinterpret_cast<const uint4*>(Wq + size_t(row) * size_t(cols) + size_t(col)))
+                      : make_uint4(0, 0, 0, 0);
+  }
+  const float s = e8m0_value(Ws[blockIdx.x]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 32 * i;
+    if (row >= rows) return;
+    uint32_t o[8];
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 lo = e4m3x2_to_f32(w[j]), hi = e4m3x2_to_f32(w[j] >> 16);
+      o[2 * j] = pack_bf16x2(lo.x * s, lo.y * s);
+      o[2 * j + 1] = pack_bf16x2(hi.x * s, hi.y * s);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(W + (size_t(row) * size_t(cols) + size_t(col)) * 2);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+}  // namespace lora

@@ -137,20 +137,23 @@ struct MapKeyHash {
 constexpr size_t kMapCache = 8192;
 thread_local std::unordered_map<MapKey, CUtensorMap, MapKeyHash> t_maps;
 
-bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
-              uint32_t box_outer, uint32_t swz_span_bytes) {
-  const MapKey k{ptr, inner, outer, ld, box_inner, box_outer, swz_span_bytes};
+// (`bytes` = bytes per element: 2 = bf16, 1 = raw bytes; in the key beside
+// the swizzle span, which is at most 128.)
+bool make_map_sized(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
+                    uint32_t box_outer, uint32_t swz_span_bytes, uint32_t bytes) {
+  const MapKey k{ptr, inner, outer, ld, box_inner, box_outer, swz_span_bytes | bytes << 16};
   const auto it = t_maps.find(k);
   if (it != t_maps.end()) {
     *m = it->second;
     return true;
   }
   cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {ld * 2};
+  cuuint64_t strides[1] = {ld * bytes};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult rc = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
-                               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz_enum(swz_span_bytes),
+  const CUtensorMapDataType type = bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult rc = g_encode(m, type, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, swz_enum(swz_span_bytes),
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (rc != CUDA_SUCCESS) {
     std::fprintf(stderr, "lora_b200: cuTensorMapEncodeTiled failed (%d) dims=%llu,%llu box=%u,%u\n", int(rc),
@@ -160,6 +163,17 @@ bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, u
   if (t_maps.size() >= kMapCache) t_maps.clear();
   t_maps.emplace(k, *m);
   return true;
+}
+
+bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
+              uint32_t box_outer, uint32_t swz_span_bytes) {
+  return make_map_sized(m, ptr, inner, outer, ld, box_inner, box_outer, swz_span_bytes, 2);
+}
+
+// The same for one-byte elements, 128-byte swizzle.
+bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
+                 uint32_t box_outer) {
+  return make_map_sized(m, ptr, inner, outer, ld, box_inner, box_outer, 128, 1);
 }
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel, device

@@ -153,6 +153,7 @@ const char* lora_status_string(lora_status_t s) {
     case LORA_ERR_UNSUPPORTED_DEVICE: return "LORA_ERR_UNSUPPORTED_DEVICE: needs an sm_100 (B200) device";
     case LORA_ERR_ALIAS: return "LORA_ERR_ALIAS: an output overlaps an input";
     case LORA_ERR_FLAGS: return "LORA_ERR_FLAGS: unknown bit in a flags argument";
+    case LORA_ERR_DROPOUT: return "LORA_ERR_DROPOUT: p outside [0, 1) or no seed and offset for p > 0";
   }
   return "LORA_ERR_UNKNOWN";
 }
@@ -875,3 +876,7 @@ extern "C" lora_status_t lora_bwd_noalloc(const void* X, const void* W, const vo
                  need > 0 ? kNoAllocScratchBytes : 0,
                  need, 0u, stream);
 }
+
+// ============================================ dropout and the 8-bit base ====
+
+#include "adapter_api.cuh"

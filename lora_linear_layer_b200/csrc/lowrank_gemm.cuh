@@ -1,0 +1,478 @@
+// lowrank_gemm.cuh - OUT = P Q + m * (U V), the products that carry an
+// adapter whose rank-side operand U is already in memory:
+//   Y  = X W^T    + T B^T           (bf16 base, T with dropout: adapter_pass.cuh)
+//   Y  = Xq Wq^T  + T B^T           (8-bit base)
+//   dX = dY W     + m * (dT A)/(1-p)
+//   dX = dYq Wq   + m * (dT A)/(1-p)
+// One accumulator holds both products.  The rank side is one or two K blocks
+// of the same ring, issued before the base blocks: where the mask m applies
+// to it alone (DROP), the epilogue warps take the rank product out of TMEM,
+// mask and scale it, and put it back, and the base product then accumulates
+// onto it.  That costs no extra accumulator and no extra pass over OUT, and
+// it hides behind another tile's K loop: the rank blocks of the next tile
+// are issued in the middle of the current one, into the other accumulator.
+//
+// FP8: operands are e4m3 with power-of-two scales for 128 values of K, which
+// is what kind::mxf8f6f4 applies itself (it takes one scale for 32 values of
+// K; the four of a block are the same byte).  A stage holds 128 values of K
+// (128-byte rows, as 64 bf16 are), so the ring, the swizzle and the
+// descriptors are those of the bf16 form.  The scales of four stages are the
+// four bytes of one 32-bit word for each row (column) of the tile, selected
+// by the scale index of the instruction descriptor: one warp builds the
+// words of a tile's 128 rows and BN columns in shared memory every four
+// stages and the MMA thread copies them to TMEM (tcgen05.cp).  Two
+// accumulators of 224 columns leave 64 columns of TMEM for them: four
+// buffers of 16 columns, and a buffer comes round again after 16 stages,
+// more than the ring has, so the MMAs that read it are done.
+//
+// Tiles are CTA pairs (cta_group::2) of 256 x BN, walked in the order of
+// fused.cuh's dX form.  What bounds it is the tensor pipe.
+#pragma once
+
+#include "common.cuh"
+#include "fused.cuh"
+#include "philox.cuh"
+
+namespace lora {
+
+constexpr int kLrScaleBufs = 4;
+constexpr uint32_t kLrScaleBytes = 512u * 3u;  // A: 128 rows, B: 256 columns, 4 bytes each
+
+struct LrArgs {
+  FusedArgs f;               // sizes, tile counts, schedule, stages, ep_bufs
+  DropArgs drop;             // DROP: the mask of OUT's [M, N]
+  const uint32_t* p_scales;  // FP8: words of 4 scale bytes, [ceil(K / 512)][M]
+  const uint8_t* q_scales;   // FP8: bytes of 128 x 128 blocks
+  int32_t qs_n, qs_k;        // their counts along N and K
+  int32_t qs_ld_n, qs_ld_k;  // and strides
+};
+
+template <bool FP8, bool MN, int BN>
+struct LrShape {
+  static constexpr int kBNC = BN / 2;                     // columns of OUT whose Q values a CTA holds
+  static constexpr int kChunks = (kBNC + 63) / 64;        // 64-column chunks of bf16 MN-major operands
+  static constexpr uint32_t kQBase = !MN ? kBNC * 128u : FP8 ? 16384u : kChunks * 8192u;  // bytes loaded, base block
+  static constexpr uint32_t kQRank = !MN ? kBNC * 128u : kChunks * 8192u;                 // bytes loaded, rank block
+  static constexpr uint32_t kQSlot = kQBase > kQRank ? kQBase : kQRank;
+  static constexpr uint32_t kStage = 16384u + kQSlot;
+  static constexpr int kThreads = FP8 ? kFusedThreads + 32 : kFusedThreads;
+};
+
+struct LrLayout {
+  uint32_t off_sf, off_ep, off_bar, total;
+  __host__ __device__ LrLayout(uint32_t stage_bytes, bool fp8, int stages, int ep_bufs) {
+    off_sf = stage_bytes * uint32_t(stages);
+    off_ep = off_sf + (fp8 ? kLrScaleBufs * kLrScaleBytes : 0u);
+    off_bar = off_ep + 4u * uint32_t(ep_bufs) * kEpBufBytes;
+    total = off_bar + 512;
+  }
+};
+
+template <bool FP8, bool MN, bool DROP, int BN>
+__global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
+    lowrank_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CUtensorMap tmO, const __grid_constant__ LrArgs la) {
+  static_assert(BN % 32 == 0 && 2 * BN + (FP8 ? 16 * kLrScaleBufs : 0) <= 512, "TMEM");
+  static_assert(!DROP || MN, "only dX masks its rank product");
+  using Sh = LrShape<FP8, MN, BN>;
+  using G = Group<2>;
+  constexpr int BNC = Sh::kBNC;
+  constexpr int kStageK = FP8 ? 128 : 64;
+  const FusedArgs& a = la.f;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (sbase - raw);
+  const LrLayout L(Sh::kStage, FP8, a.stages, a.ep_bufs);
+  const int S = a.stages;
+  const uint32_t bar0 = sbase + L.off_bar;
+  // full, accempty, masked, sffull and drain are used on the even CTA only
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  const uint32_t accfull0 = bar0 + 8u * (2 * S);        // +8*b
+  const uint32_t accempty0 = bar0 + 8u * (2 * S + 2);   // +8*b
+  const uint32_t rankfull = bar0 + 8u * (2 * S + 4);    // DROP: a rank product is in its accumulator
+  const uint32_t masked = bar0 + 8u * (2 * S + 5);      // DROP: ... and masked
+  const uint32_t drain = bar0 + 8u * (2 * S + 6);
+  const uint32_t sffull0 = bar0 + 8u * (2 * S + 7);     // +8*buf
+  const uint32_t sfempty0 = sffull0 + 8u * kLrScaleBufs;
+  uint32_t* const tmem_slot =
+      reinterpret_cast<uint32_t*>(gbase + L.off_bar + 8 * (2 * S + 7 + 2 * kLrScaleBufs));
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accfull0 + 8u * b, 1);
+      mbar_init(accempty0 + 8u * b, 8);
+    }
+    mbar_init(rankfull, 1);
+    mbar_init(masked, 8);
+    mbar_init(drain, 1);
+    for (int i = 0; i < kLrScaleBufs; ++i) {
+      mbar_init(sffull0 + 8u * i, 2);
+      mbar_init(sfempty0 + 8u * i, 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmU);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 2 && lane == 0) tma_prefetch_desc(&tmO);
+  if (warp == 1) G::alloc(smem_addr(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  G::cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int nk = (a.K + kStageK - 1) / kStageK;
+  const int nr = (a.r_pad + 63) / 64;  // rank blocks
+  // DROP: the next tile's rank blocks go before this base block
+  const int ahead = nk / 2;
+  const uint64_t lim = a.wait_limit_ns;
+  const int n_clusters = int(gridDim.x) / 2;
+  const int cluster_id = int(blockIdx.x) / 2;
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer ----
+    if (lane == 0) {
+      TileSched sch(a, n_clusters, cluster_id);
+      int stage = 0;
+      uint32_t phase = 0;
+      auto claim = [&](uint32_t bytes, uint32_t& st, uint32_t& fb) -> bool {
+        if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, lim, SITE_EMPTY, true)) return false;
+        st = sbase + uint32_t(stage) * Sh::kStage;
+        fb = G::leader_addr(full_bar(stage));
+        if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * (16384u + bytes));
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+        return true;
+      };
+      auto rank_blocks = [&](int m, int n) -> bool {
+        const int row0 = m * 256 + int(rank) * kBM;
+        const int q0 = n * BN + int(rank) * BNC;
+        for (int rb = 0; rb < nr; ++rb) {
+          uint32_t st, fb;
+          if (!claim(Sh::kQRank, st, fb)) return false;
+          G::load(st, &tmU, fb, rb * 64, row0);
+          if constexpr (!MN) {
+            G::load(st + 16384u, &tmV, fb, rb * 64, q0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < Sh::kChunks; ++i)
+              G::load(st + 16384u + uint32_t(i) * 8192u, &tmV, fb, q0 + 64 * i, rb * 64);
+          }
+        }
+        return true;
+      };
+      auto base_blocks = [&](int m, int n, int from, int to) -> bool {
+        const int row0 = m * 256 + int(rank) * kBM;
+        const int q0 = n * BN + int(rank) * BNC;
+        for (int kb = from; kb < to; ++kb) {
+          uint32_t st, fb;
+          if (!claim(Sh::kQBase, st, fb)) return false;
+          const int k0 = kb * kStageK;
+          G::load(st, &tmP, fb, k0, row0);
+          if constexpr (!MN) {
+            G::load(st + 16384u, &tmQ, fb, k0, q0);
+          } else if constexpr (FP8) {
+            G::load(st + 16384u, &tmQ, fb, q0, k0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < Sh::kChunks; ++i)
+              G::load(st + 16384u + uint32_t(i) * 8192u, &tmQ, fb, q0 + 64 * i, k0);
+          }
+        }
+        return true;
+      };
+      int m, n, mn = 0, nn = 0;
+      bool have = sch.next(m, n);
+      bool ok = !(DROP && have) || rank_blocks(m, n);
+      while (ok && have) {
+        const bool more = sch.next(mn, nn);
+        if constexpr (DROP) {
+          ok = base_blocks(m, n, 0, ahead) && (!more || rank_blocks(mn, nn)) && base_blocks(m, n, ahead, nk);
+        } else {
+          ok = rank_blocks(m, n) && base_blocks(m, n, 0, nk);
+        }
+        m = mn;
+        n = nn;
+        have = more;
+      }
+      if (*abort_flag) settle_ns(200000);  // let copies in flight land
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------- MMA issuer ----
+    if (lane == 0 && leader) {
+      const uint32_t id_base = idesc_bf16(256, BN, false, MN);  // also the rank blocks' (V has Q's layout)
+      TileSched sch(a, n_clusters, cluster_id);
+      int stage = 0;
+      uint32_t phase = 0, sf_n = 0, marks = 0;
+      uint32_t acc_waits[2] = {0u, 0u};
+      auto take = [&](uint32_t& st) -> bool {
+        if (!wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL, true)) return false;
+        tc_fence_after();
+        st = sbase + uint32_t(stage) * Sh::kStage;
+        return true;
+      };
+      auto give = [&]() {
+        G::commit_all(empty_bar(stage));
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      };
+      // waits for the accumulator and starts it with the rank product
+      auto rank_blocks = [&](uint32_t b) -> bool {
+        const uint32_t w = b ? acc_waits[1]++ : acc_waits[0]++;
+        if (!wait_bounded(accempty0 + 8u * b, (w & 1u) ^ 1u, abort_flag, lim, SITE_ACCEMPTY, true)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + b * BN;
+        for (int rb = 0; rb < nr; ++rb) {
+          uint32_t st;
+          if (!take(st)) return false;
+          const uint32_t sq = st + 16384u;
+          const int kk_n = imin(4, (a.r_pad - rb * 64) / 16);
+          for (int kk = 0; kk < kk_n; ++kk)
+            G::mma(d, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
+                   MN ? smem_desc(sq + kk * 2048u, 8192u, 1024u, SWZ_128B)
+                      : smem_desc(sq + kk * 32u, 16u, 1024u, SWZ_128B),
+                   id_base, (rb | kk) != 0);
+          give();
+        }
+        if constexpr (DROP) G::commit_all(rankfull);
+        return true;
+      };
+      auto base_blocks = [&](uint32_t b, int from, int to) -> bool {
+        const uint32_t d = tmem + b * BN;
+        uint32_t sf_tmem = 0;
+        if constexpr (FP8) sf_tmem = tmem + 2 * BN + 16u * ((sf_n - 1u) % kLrScaleBufs);
+        for (int kb = from; kb < to; ++kb) {
+          uint32_t st;
+          if (!take(st)) return false;
+          const uint32_t sq = st + 16384u;
+          if constexpr (FP8) {
+            if ((kb & 3) == 0) {
+              const uint32_t buf = sf_n % kLrScaleBufs, par = (sf_n / kLrScaleBufs) & 1u;
+              ++sf_n;
+              if (!wait_bounded(sffull0 + 8u * buf, par, abort_flag, lim, SITE_TXMSG, true)) return false;
+              tc_fence_after();
+              sf_tmem = tmem + 2 * BN + 16u * buf;
+              const uint32_t src = sbase + L.off_sf + buf * kLrScaleBytes;
+#pragma unroll
+              for (uint32_t i = 0; i < 3; ++i)
+                tmem_cp_scales_pair(sf_tmem + 4u * i, smem_desc(src + 512u * i, 16u, 128u, SWZ_NONE));
+              G::commit_all(sfempty0 + 8u * buf);
+            }
+            const uint32_t id = idesc_mxf8(256, BN, false, MN, uint32_t(kb & 3));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_mxf8_pair(d, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
+                             MN ? smem_desc(sq + kk * 4096u, 16384u, 1024u, SWZ_128B)
+                                : smem_desc(sq + kk * 32u, 16u, 1024u, SWZ_128B),
+                             id, sf_tmem, sf_tmem + 4u, 1u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              G::mma(d, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
+                     MN ? smem_desc(sq + kk * 2048u, 8192u, 1024u, SWZ_128B)
+                        : smem_desc(sq + kk * 32u, 16u, 1024u, SWZ_128B),
+                     id_base, 1u);
+          }
+          give();
+        }
+        return true;
+      };
+      int m, n;
+      bool have = sch.next(m, n);
+      uint32_t b = 0;
+      bool ok = !(DROP && have) || rank_blocks(0);
+      while (ok && have) {
+        const bool more = sch.next(m, n);
+        if constexpr (DROP) {
+          ok = wait_bounded(masked, marks++ & 1u, abort_flag, lim, SITE_STFULL, true);
+          tc_fence_after();
+          ok = ok && base_blocks(b, 0, ahead) && (!more || rank_blocks(b ^ 1u)) && base_blocks(b, ahead, nk);
+        } else {
+          ok = rank_blocks(b) && base_blocks(b, 0, nk);
+        }
+        if (!ok) break;
+        G::commit_all(accfull0 + 8u * b);
+        b ^= 1u;
+        have = more;
+      }
+      // make sure no tcgen05 op is still running before TMEM is released
+      G::commit_local(drain);
+      wait_bounded(drain, 0u, abort_flag, lim, SITE_DRAIN, false);
+    }
+  } else if (warp < 6) {
+    // ---------------------------------------------------- epilogue ----
+    const int q = warp & 3;            // TMEM lane quarter of this warp
+    const uint32_t lane_base = uint32_t(q * 32) << 16;
+    TileSched sch(a, n_clusters, cluster_id);
+    uint32_t ranks = 0, full_waits[2] = {0u, 0u};
+    const uint32_t ep_off = L.off_ep + uint32_t(q * a.ep_bufs) * kEpBufBytes;
+    uint32_t epc = 0;  // output blocks staged so far
+    DropState ds{};
+    if constexpr (DROP) ds = drop_load(la.drop);
+    // DROP: mask and scale the rank product in accumulator b, tile (m, n)
+    auto mask_tile = [&](uint32_t b, int m, int n) -> bool {
+      if (!warp_wait_bounded(rankfull, ranks++ & 1u, abort_flag, lim, SITE_TFULL, true)) return false;
+      tc_fence_after();
+      const uint32_t row = uint32_t(m * 256 + int(rank) * kBM + q * 32 + lane);
+#pragma unroll 1
+      for (int ch = 0; ch < BN / 32; ++ch) {
+        const uint32_t col = tmem + lane_base + b * BN + uint32_t(ch * 32);
+        uint32_t v[32];
+        tmem_ld_x32(col, v);
+        const uint32_t c8 = uint32_t(n * BN + ch * 32) / 8u;
+        uint4 r[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) r[g] = drop_block(ds, c8 + g, row);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t w[4] = {r[g].x, r[g].y, r[g].z, r[g].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = __uint_as_float(v[8 * g + 2 * i]) * la.drop.inv_keep;
+            const float hi = __uint_as_float(v[8 * g + 2 * i + 1]) * la.drop.inv_keep;
+            v[8 * g + 2 * i] = (w[i] << 16) < ds.thr_hi ? 0u : __float_as_uint(lo);
+            v[8 * g + 2 * i + 1] = w[i] < ds.thr_hi ? 0u : __float_as_uint(hi);
+          }
+        }
+        tmem_st_x32(col, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) G::arrive_leader(masked);
+      return true;
+    };
+    int m, n, mn = 0, nn = 0;
+    bool have = sch.next(m, n);
+    uint32_t b = 0;
+    bool ok = true;
+    if constexpr (DROP) ok = !have || mask_tile(0, m, n);
+    while (ok && have) {
+      const bool more = sch.next(mn, nn);
+      if constexpr (DROP) {
+        if (more && !mask_tile(b ^ 1u, mn, nn)) break;
+      }
+      const uint32_t fpar = (b ? full_waits[1]++ : full_waits[0]++) & 1u;
+      if (!warp_wait_bounded(accfull0 + 8u * b, fpar, abort_flag, lim, SITE_ACCFULL, true)) break;
+      tc_fence_after();
+      const int wrow0 = m * 256 + int(rank) * kBM + q * 32;
+#pragma unroll 1
+      for (int ch = 0; ch < BN / kEpCols; ++ch) {
+        uint32_t v[32];
+        tmem_ld_x32(tmem + lane_base + b * BN + uint32_t(ch * kEpCols), v);
+        tmem_ld_wait();
+        const int col0 = n * BN + ch * kEpCols;
+        if (col0 >= a.N || wrow0 >= a.M) continue;
+        uint4 pk[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          pk[g].x = pack_bf16x2(__uint_as_float(v[8 * g + 0]), __uint_as_float(v[8 * g + 1]));
+          pk[g].y = pack_bf16x2(__uint_as_float(v[8 * g + 2]), __uint_as_float(v[8 * g + 3]));
+          pk[g].z = pack_bf16x2(__uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
+          pk[g].w = pack_bf16x2(__uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
+        }
+        // the store that last used this buffer has read it
+        if (lane == 0) {
+          if (a.ep_bufs == 2) bulk_wait_group_read1();
+          else bulk_wait_group_read0();
+        }
+        __syncwarp();
+        const uint32_t bo = ep_off + (a.ep_bufs == 2 ? (epc & 1u) * kEpBufBytes : 0u);
+        ++epc;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<uint4*>(gbase + bo + swz_offset(uint32_t(lane), uint32_t(g), kEpCols * 2)) = pk[g];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tmO, sbase + bo, col0, wrow0);
+          bulk_commit_group();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) G::arrive_leader(accempty0 + 8u * b);
+      b ^= 1u;
+      m = mn;
+      n = nn;
+      have = more;
+    }
+    if (lane == 0) bulk_wait_group0();  // every output store has completed
+  } else if constexpr (FP8) {
+    // ------------------------------------------------ scale builder ----
+    TileSched sch(a, n_clusters, cluster_id);
+    const int groups = (nk + 3) / 4;
+    uint32_t sf_n = 0;
+    int m, n;
+    bool ok = true;
+    while (ok && sch.next(m, n)) {
+      const int row0 = m * 256 + int(rank) * kBM + lane;
+      // byte lane & 3 of column word lane >> 2
+      const int nb = imin((n * BN + 32 * (lane >> 2)) >> 7, la.qs_n - 1);
+      const uint8_t* const qs = la.q_scales + size_t(nb) * size_t(la.qs_ld_n);
+      auto fetch = [&](int g, uint32_t (&pa)[4], uint32_t& qb) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pa[i] = la.p_scales[size_t(g) * size_t(a.M) + size_t(imin(row0 + 32 * i, a.M - 1))];
+        qb = qs[size_t(imin(4 * g + (lane & 3), la.qs_k - 1)) * size_t(la.qs_ld_k)];
+      };
+      uint32_t pa[4], qb, pa_next[4] = {0, 0, 0, 0}, qb_next = 0;
+      fetch(0, pa, qb);
+      for (int g = 0; g < groups; ++g) {
+        if (g + 1 < groups) fetch(g + 1, pa_next, qb_next);
+        const uint32_t buf = sf_n % kLrScaleBufs, par = (sf_n / kLrScaleBufs) & 1u;
+        ++sf_n;
+        if (!warp_wait_bounded(sfempty0 + 8u * buf, par ^ 1u, abort_flag, lim, SITE_VEMPTY, true)) {
+          ok = false;
+          break;
+        }
+        uint32_t v = qb << (8 * (lane & 3));
+        v |= __shfl_xor_sync(0xffffffffu, v, 1);
+        v |= __shfl_xor_sync(0xffffffffu, v, 2);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __shfl_sync(0xffffffffu, v, 4 * i);
+        const uint32_t dst = sbase + L.off_sf + buf * kLrScaleBytes + 16u * uint32_t(lane);
+        st_shared_v4(dst, make_uint4(pa[0], pa[1], pa[2], pa[3]));
+        st_shared_v4(dst + 512u, make_uint4(w[0], w[1], w[2], w[3]));
+        st_shared_v4(dst + 1024u, make_uint4(w[4], w[5], w[6], w[7]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) G::arrive_leader(sffull0 + 8u * buf);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pa[i] = pa_next[i];
+        qb = qb_next;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  G::cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    G::dealloc(tmem, 512);
+  }
+}
+
+}  // namespace lora
