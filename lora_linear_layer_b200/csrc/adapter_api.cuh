@@ -5,6 +5,7 @@
 
 #include "adapter_pass.cuh"
 #include "lowrank_gemm.cuh"
+#include "token.cuh"
 
 namespace {
 
@@ -34,17 +35,21 @@ lora_status_t check_sizes_fp8(int64_t M, int64_t d_in, int64_t d_out, int32_t r)
 }
 
 // The 8-bit layer's workspace: T and dT as the backward's, then the codes of
-// X or dY and their scales.
+// X or dY, their scales and the weight's as the product reads them.
 struct Fp8Workspace {
-  size_t off_codes, off_scales, total;
+  size_t off_codes, off_scales, off_atoms, total;
 };
+
+// Scale atoms of a product's N columns (tiles are at least 128 wide) over K.
+size_t atom_bytes(int64_t N, int64_t K) { return size_t((N + 127) / 128) * size_t((K + 511) / 512) * 1024; }
 
 Fp8Workspace fp8_workspace(int64_t M, int64_t d_in, int64_t d_out, int32_t r) {
   const size_t wide = size_t(std::max(d_in, d_out));
   Fp8Workspace w;
   w.off_codes = bwd_workspace(M, r).total;
   w.off_scales = w.off_codes + align256(size_t(M) * wide);
-  w.total = w.off_scales + align256(size_t(M) * ((wide + 511) / 512) * 4);
+  w.off_atoms = w.off_scales + size_t((M + 127) / 128) * ((wide + 511) / 512) * 512;
+  w.total = w.off_atoms + std::max(atom_bytes(d_out, d_in), atom_bytes(d_in, d_out));
   return w;
 }
 
@@ -106,9 +111,11 @@ struct PassMaps {
   CUtensorMap p, r;
 };
 
+constexpr int kAtomBlocks = 16;  // blocks (times the splits) that lay out the weight's scales
+
 template <bool P_MN, int RCW, bool QUANT>
 lora_status_t launch_pass_t(const PassMaps& m0, const PassCfg& c0, const PassMaps* m1, const PassCfg* c1,
-                            cudaStream_t st) {
+                            const ScaleAtomArgs& atoms, cudaStream_t st) {
   auto kern = adapter_pass_kernel<P_MN, RCW, QUANT>;
   const uint32_t smem = c1 != nullptr ? std::max(c0.smem, c1->smem) : c0.smem;
   if (!ensure_smem_attr(kern, smem)) return LORA_ERR_CUDA;
@@ -116,34 +123,43 @@ lora_status_t launch_pass_t(const PassMaps& m0, const PassCfg& c0, const PassMap
   const int t1 = c1 != nullptr ? int((int64_t(c1->args.rows) + 127) / 128) : 0;
   const dim3 cl(1, unsigned(c0.args.splits), 1);
   const PassMaps& second = m1 != nullptr ? *m1 : m0;
-  return launch_ex("adapter pass", kern, dim3(unsigned(t0 + t1), unsigned(c0.args.splits)), dim3(kPassThreads), smem,
-                   st, &cl, m0.p, m0.r, second.p, second.r, c0.args, c1 != nullptr ? c1->args : c0.args, int32_t(t0));
+  const int ta = atoms.bytes != nullptr ? kAtomBlocks : 0;
+  return launch_ex("adapter pass", kern, dim3(unsigned(t0 + t1 + ta), unsigned(c0.args.splits)), dim3(kPassThreads),
+                   smem, st, &cl, m0.p, m0.r, second.p, second.r, c0.args, c1 != nullptr ? c1->args : c0.args,
+                   int32_t(t0), int32_t(t0 + t1), atoms);
 }
 
 template <bool P_MN, bool QUANT>
 lora_status_t launch_pass(const PassMaps& m0, const PassCfg& c0, cudaStream_t st, const PassMaps* m1 = nullptr,
-                          const PassCfg* c1 = nullptr) {
-  if (c0.RCW == 16) return launch_pass_t<P_MN, 16, QUANT>(m0, c0, m1, c1, st);
-  if (c0.RCW == 32) return launch_pass_t<P_MN, 32, QUANT>(m0, c0, m1, c1, st);
-  return launch_pass_t<P_MN, 64, QUANT>(m0, c0, m1, c1, st);
+                          const PassCfg* c1 = nullptr, const ScaleAtomArgs& atoms = ScaleAtomArgs{}) {
+  if (c0.RCW == 16) return launch_pass_t<P_MN, 16, QUANT>(m0, c0, m1, c1, atoms, st);
+  if (c0.RCW == 32) return launch_pass_t<P_MN, 32, QUANT>(m0, c0, m1, c1, atoms, st);
+  return launch_pass_t<P_MN, 64, QUANT>(m0, c0, m1, c1, atoms, st);
 }
 
-// T = scale (m * X) A^T into `Tws`; with `codes`, X's codes and scales too.
+// What a pass over an 8-bit layer's operand leaves for the product.
+struct Rounded {
+  uint8_t* codes;
+  uint8_t* scales;
+  ScaleAtomArgs atoms;  // the weight's scales, to be laid out beside
+};
+
+// T = scale (m * X) A^T into `Tws`; with `q`, X's codes and scales too.
 lora_status_t launch_down(const void* X, const void* A, int64_t M, int64_t d_in, int32_t r, float scale,
-                          const DropArgs& drop, __nv_bfloat16* Tws, uint8_t* codes, uint8_t* scales, int sm_count,
-                          cudaStream_t st) {
+                          const DropArgs& drop, __nv_bfloat16* Tws, const Rounded* q, int sm_count, cudaStream_t st) {
   PassCfg c;
   pick_pass(M, d_in, r, false, false, OUT_ROWS_RPAD, (M + 127) / 128, sm_count, c);
   c.args.out = Tws;
   c.args.scale = scale * drop.inv_keep;
   c.args.drop = drop;
-  c.args.codes = codes;
-  c.args.scales = scales;
   PassMaps m;
   if (!make_map(&m.p, X, d_in, M, d_in, 64, 128, 128) ||
       !make_map(&m.r, A, d_in, r, d_in, 64, uint32_t(c.args.r_pad), 128))
     return LORA_ERR_CUDA;
-  return codes != nullptr ? launch_pass<false, true>(m, c, st) : launch_pass<false, false>(m, c, st);
+  if (q == nullptr) return launch_pass<false, false>(m, c, st);
+  c.args.codes = q->codes;
+  c.args.scales = q->scales;
+  return launch_pass<false, true>(m, c, st, nullptr, nullptr, q->atoms);
 }
 
 // -------------------------------------------------------- low-rank GEMMs ----
@@ -164,20 +180,20 @@ uint32_t lr_stage_bytes(bool fp8, bool mn, int BN) {
 }
 
 // OUT[M, N] over the contraction K: the wide tile (224 columns for 8 bits,
-// 256 for bf16) unless 128-wide ones, each with its share of fixed cost (32
-// columns' worth), finish sooner.
+// 256 for bf16) unless 128-wide ones finish sooner, at a cost of FIX columns
+// more each.
 void pick_lr(int64_t M, int64_t N, int64_t K, int r, bool fp8, bool mn, int sm_count, LrCfg& c) {
   const int64_t clusters = sm_count / 2;
   const int64_t num_m = (M + 255) / 256;
   auto cost = [&](int bn) {
     const int64_t tiles = num_m * ((N + bn - 1) / bn);
-    return ((tiles + clusters - 1) / clusters) * int64_t(bn + 32);
+    return ((tiles + clusters - 1) / clusters) * int64_t(bn + 64);
   };
   const int wide = fp8 ? 224 : 256;
   c.BN = cost(128) < cost(wide) ? 128 : wide;
   const uint32_t stage = lr_stage_bytes(fp8, mn, c.BN);
   auto stages_for = [&](int ep_bufs) {
-    return std::min(8, int((kSmemMax - LrLayout(stage, fp8, 0, ep_bufs).total - 1024) / stage));
+    return std::min(fp8 ? kLrMaxStagesFp8 : 8, int((kSmemMax - LrLayout(stage, fp8, 0, ep_bufs).total - 1024) / stage));
   };
   std::memset(&c.args, 0, sizeof(c.args));
   FusedArgs& a = c.args.f;
@@ -191,9 +207,10 @@ void pick_lr(int64_t M, int64_t N, int64_t K, int r, bool fp8, bool mn, int sm_c
   a.scale = 1.0f;
   a.num_m = int32_t(num_m);
   a.num_n = int32_t((N + c.BN - 1) / c.BN);
-  a.band_w = a.num_n;  // single-tile runs dealt round-robin use no bands
-  a.n_bands = 1;
-  a.run_l = 1;
+  // as many M blocks together as keep their rows of P in about a third of
+  // the 126 MB L2
+  const int64_t block_bytes = 256 * K * (fp8 ? 1 : 2);
+  c.args.group_m = int32_t(std::max<int64_t>(1, std::min<int64_t>({num_m, 16, (int64_t(40) << 20) / block_bytes})));
   a.wait_limit_ns = kWaitLimitNs;
   c.args.drop = DropArgs{nullptr, 0u, 1.0f};
 }
@@ -205,8 +222,8 @@ lora_status_t launch_lr_t(const CUtensorMap* maps, const LrCfg& c, int sm_count,
   const int64_t tiles = int64_t(c.args.f.num_m) * c.args.f.num_n;
   const int clusters = int(std::min<int64_t>(tiles, max_clusters(kern, 2, c.smem, sm_count)));
   const dim3 cl(2, 1, 1);
-  return launch_ex("low-rank GEMM", kern, dim3(unsigned(clusters * 2)), dim3(LrShape<FP8, MN, BN>::kThreads), c.smem,
-                   st, &cl, maps[0], maps[1], maps[2], maps[3], maps[4], c.args);
+  return launch_ex("low-rank GEMM", kern, dim3(unsigned(clusters * 2)), dim3(kFusedThreads), c.smem, st, &cl,
+                   maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], c.args);
 }
 
 template <bool MN, bool DROP>
@@ -218,69 +235,166 @@ lora_status_t launch_lr(bool fp8, const CUtensorMap* maps, const LrCfg& c, int s
                      : launch_lr_t<false, MN, DROP, 128>(maps, c, sm_count, st);
 }
 
+// The product's view of the weight's scales: columns of the forward are rows
+// of W, those of dX columns.
+ScaleAtomArgs scale_atom_args(const Base& W, const Rounded& q, const LrCfg& c, bool mn, int64_t d_in, int64_t d_out) {
+  ScaleAtomArgs a;
+  const int32_t out_b = int32_t(qblocks(d_out)), in_b = int32_t(qblocks(d_in));
+  a.bytes = reinterpret_cast<const uint8_t*>(W.scales);
+  a.atoms = q.atoms.atoms;
+  a.tiles = c.args.f.num_n;
+  a.groups = (c.args.f.K + 511) / 512;
+  a.bn = c.BN;
+  a.n_blocks = mn ? in_b : out_b;
+  a.k_blocks = mn ? out_b : in_b;
+  a.ld_n = mn ? 1 : in_b;
+  a.ld_k = mn ? in_b : 1;
+  return a;
+}
+
+bool scale_maps(CUtensorMap* maps, const Rounded& q, const LrCfg& c) {
+  const uint64_t groups = uint64_t((c.args.f.K + 511) / 512);
+  return make_map_atoms(&maps[0], q.scales, groups * uint64_t((c.args.f.M + 127) / 128), 1) &&
+         make_map_atoms(&maps[1], q.atoms.atoms, groups * uint64_t(c.args.f.num_n) * 2, 2);
+}
+
 // Y = X W^T + T B^T from T (bf16 [M, r_pad], scale included); for an 8-bit
-// base X is its codes, with `x_scales`.
-lora_status_t launch_up(const void* X, const uint8_t* x_scales, const Base& W, const void* B, void* Y,
-                        const __nv_bfloat16* Tws, int64_t M, int64_t d_in, int64_t d_out, int32_t r, int sm_count,
-                        cudaStream_t st) {
-  LrCfg c;
+// base from X's codes in `q`.
+lora_status_t launch_up(const void* X, const Rounded& q, const Base& W, const void* B, void* Y,
+                        const __nv_bfloat16* Tws, const LrCfg& c, int32_t r, int sm_count, cudaStream_t st) {
+  const int64_t M = c.args.f.M, d_in = c.args.f.K, d_out = c.args.f.N;
   const bool fp8 = W.fp8();
-  pick_lr(M, d_out, d_in, r, fp8, false, sm_count, c);
-  c.args.f.out = reinterpret_cast<__nv_bfloat16*>(Y);
   const uint32_t bnc = uint32_t(c.BN / 2);
   const uint64_t r_pad = uint64_t(r_pad_of(r));
-  CUtensorMap maps[5];
-  const bool ok = fp8 ? make_map_u8(&maps[0], X, d_in, M, d_in, 128, 128) &&
-                            make_map_u8(&maps[1], W.w, d_in, d_out, d_in, 128, bnc)
+  CUtensorMap maps[7];
+  const bool ok = fp8 ? make_map_u8(&maps[0], q.codes, d_in, M, d_in, 128, 128) &&
+                            make_map_u8(&maps[1], W.w, d_in, d_out, d_in, 128, bnc) && scale_maps(maps + 5, q, c)
                       : make_map(&maps[0], X, d_in, M, d_in, 64, 128, 128) &&
                             make_map(&maps[1], W.w, d_in, d_out, d_in, 64, bnc, 128);
   if (!ok || !make_map(&maps[2], Tws, r_pad, M, r_pad, 64, 128, 128) ||
       !make_map(&maps[3], B, r, d_out, r, 64, bnc, 128) ||
       !make_map(&maps[4], Y, d_out, M, d_out, kEpCols, 32, kEpCols * 2))
     return LORA_ERR_CUDA;
-  if (fp8) {
-    c.args.p_scales = reinterpret_cast<const uint32_t*>(x_scales);
-    c.args.q_scales = reinterpret_cast<const uint8_t*>(W.scales);
-    c.args.qs_n = int32_t(qblocks(d_out));
-    c.args.qs_k = int32_t(qblocks(d_in));
-    c.args.qs_ld_n = c.args.qs_k;
-    c.args.qs_ld_k = 1;
-  }
+  if (!fp8) maps[5] = maps[6] = maps[0];  // (unused)
   return launch_lr<false, false>(fp8, maps, c, sm_count, st);
 }
 
-// dX = dY W + m * (dT A)/(1-p).
-lora_status_t launch_dx(const void* dY, const uint8_t* dy_scales, const Base& W, const void* A, void* dX,
-                        const __nv_bfloat16* dTws, int64_t M, int64_t d_in, int64_t d_out, int32_t r,
-                        const DropArgs& drop, int sm_count, cudaStream_t st) {
-  LrCfg c;
+// dX = dY W + m * (dT A)/(1-p); for an 8-bit base from dY's codes in `q`.
+lora_status_t launch_dx(const void* dY, const Rounded& q, const Base& W, const void* A, void* dX,
+                        const __nv_bfloat16* dTws, const LrCfg& c, int32_t r, int sm_count, cudaStream_t st) {
+  const int64_t M = c.args.f.M, d_in = c.args.f.N, d_out = c.args.f.K;
   const bool fp8 = W.fp8();
-  pick_lr(M, d_in, d_out, r, fp8, true, sm_count, c);
-  c.args.f.out = reinterpret_cast<__nv_bfloat16*>(dX);
-  c.args.drop = drop;
   const uint64_t r_pad = uint64_t(r_pad_of(r));
-  CUtensorMap maps[5];
-  const bool ok = fp8 ? make_map_u8(&maps[0], dY, d_out, M, d_out, 128, 128) &&
-                            make_map_u8(&maps[1], W.w, d_in, d_out, d_in, 128, 128)
+  CUtensorMap maps[7];
+  const bool ok = fp8 ? make_map_u8(&maps[0], q.codes, d_out, M, d_out, 128, 128) &&
+                            make_map_u8(&maps[1], W.w, d_in, d_out, d_in, 128, 128) && scale_maps(maps + 5, q, c)
                       : make_map(&maps[0], dY, d_out, M, d_out, 64, 128, 128) &&
                             make_map(&maps[1], W.w, d_in, d_out, d_in, 64, 64, 128);
   if (!ok || !make_map(&maps[2], dTws, r_pad, M, r_pad, 64, 128, 128) ||
       !make_map(&maps[3], A, d_in, r, d_in, 64, 64, 128) ||
       !make_map(&maps[4], dX, d_in, M, d_in, kEpCols, 32, kEpCols * 2))
     return LORA_ERR_CUDA;
-  if (fp8) {
-    c.args.p_scales = reinterpret_cast<const uint32_t*>(dy_scales);
-    c.args.q_scales = reinterpret_cast<const uint8_t*>(W.scales);
-    c.args.qs_n = int32_t(qblocks(d_in));
-    c.args.qs_k = int32_t(qblocks(d_out));
-    c.args.qs_ld_n = 1;
-    c.args.qs_ld_k = c.args.qs_n;
-  }
-  return drop.rng != nullptr ? launch_lr<true, true>(fp8, maps, c, sm_count, st)
-                             : launch_lr<true, false>(fp8, maps, c, sm_count, st);
+  if (!fp8) maps[5] = maps[6] = maps[0];  // (unused)
+  return c.args.drop.rng != nullptr ? launch_lr<true, true>(fp8, maps, c, sm_count, st)
+                                    : launch_lr<true, false>(fp8, maps, c, sm_count, st);
+}
+
+// -------------------------------------------------------------- tokens ----
+
+// Whether launch_prep is used: its blocks read X again for every 16 rank
+// rows, which costs less than the pass's long prologue and few blocks up to
+// M * r_pad = 8192 (X[512, 8192] at r = 16: 14 against 18 us; at M = 1024 they
+// tie, and X[512, 4096] at r = 128 takes 29 against 17 us).
+bool use_prep(int64_t M, int32_t r, const DropArgs& drop) { return drop.rng == nullptr && M * r_pad_of(r) <= 8192; }
+
+// T and the codes of X for few tokens, without dropout.
+lora_status_t launch_prep(const void* X, const void* A, int64_t M, int64_t d_in, int32_t r, float scale,
+                          __nv_bfloat16* Tws, const Rounded& q, cudaStream_t st) {
+  PrepArgs p;
+  p.X = reinterpret_cast<const uint8_t*>(X);
+  p.A = reinterpret_cast<const uint8_t*>(A);
+  p.T = Tws;
+  p.codes = q.codes;
+  p.scales = q.scales;
+  p.atoms = q.atoms;
+  p.M = int32_t(M);
+  p.K = int32_t(d_in);
+  p.r = r;
+  p.r_pad = r_pad_of(r);
+  p.t_blocks = kPrepSplits * (p.r_pad / kPrepRanks) * ((p.M + kPrepTokens - 1) / kPrepTokens);
+  p.scale = scale;
+  auto blocks = [](int64_t items) {  // whole clusters of blocks, a warp an item
+    return (items + kPrepWarps * kPrepSplits - 1) / (kPrepWarps * kPrepSplits) * kPrepSplits;
+  };
+  p.q_blocks = int32_t(blocks(M * ((d_in + 511) / 512)));
+  const int64_t a_blocks = q.atoms.bytes != nullptr ? blocks(int64_t(q.atoms.tiles) * q.atoms.groups * 2) : 0;
+  const unsigned grid = unsigned(p.t_blocks + p.q_blocks + a_blocks);
+  const dim3 cl(kPrepSplits, 1, 1);
+  return launch_ex("token prep", token_prep_kernel, dim3(grid), dim3(kPrepThreads), 0, st, &cl, p);
+}
+
+// Y over an 8-bit base for at most kStreamMax tokens from what launch_prep
+// left.
+lora_status_t launch_stream(const Base& W, const void* B, void* Y, int64_t M, int64_t d_in, int64_t d_out, int32_t r,
+                            const __nv_bfloat16* Tws, const uint8_t* codes, const uint8_t* scales, int sm_count,
+                            cudaStream_t st) {
+  StreamArgs a;
+  a.Ws = reinterpret_cast<const uint8_t*>(W.scales);
+  a.x_scales = reinterpret_cast<const uint32_t*>(scales);
+  a.Y = reinterpret_cast<__nv_bfloat16*>(Y);
+  a.M = int32_t(M);
+  a.N = int32_t(d_out);
+  a.K = int32_t(d_in);
+  a.r_pad = r_pad_of(r);
+  a.tok_pad = (a.M + 15) / 16 * 16;
+  const uint32_t stage = StreamLayout(a.tok_pad, 0).stage_bytes;
+  const uint32_t fixed = kStreamScaleBufs * kStreamScaleBytes + 2048;
+  // two blocks an SM where four stages fit in half of it
+  const uint32_t half = kSmemPerSM / 2 - 1024 - fixed;
+  a.stages = std::min(8, int((half / stage >= 4 ? half : kSmemMax - fixed) / stage));
+  const uint32_t smem = StreamLayout(a.tok_pad, a.stages).total + 1024;
+  const int per_sm = std::max(1, std::min(int(kSmemPerSM / (smem + 1024)), int(512 / stream_tmem_cols(a.tok_pad))));
+  const int tiles = int((d_out + 127) / 128), nk = int((d_in + 127) / 128);
+  int splits = std::max(1, std::min({8, per_sm * sm_count / tiles, nk / 2}));
+  a.kb_per_split = (nk + splits - 1) / splits;
+  a.splits = (nk + a.kb_per_split - 1) / a.kb_per_split;
+  a.wait_limit_ns = kWaitLimitNs;
+  CUtensorMap mw, mx, mb, mt;
+  if (!make_map_u8(&mw, W.w, d_in, d_out, d_in, 128, 128) ||
+      !make_map_u8(&mx, codes, d_in, M, d_in, 128, uint32_t(a.tok_pad)) ||
+      !make_map(&mb, B, r, d_out, r, 64, 128, 128) ||
+      !make_map(&mt, Tws, uint64_t(a.r_pad), M, uint64_t(a.r_pad), 64, uint32_t(a.tok_pad), 128))
+    return LORA_ERR_CUDA;
+  if (!ensure_smem_attr(token_stream_kernel, smem)) return LORA_ERR_CUDA;
+  const dim3 cl(1, unsigned(a.splits), 1);
+  return launch_ex("token stream", token_stream_kernel, dim3(unsigned(tiles), unsigned(a.splits)),
+                   dim3(kStreamThreads), smem, st, &cl, mw, mx, mb, mt, a);
 }
 
 // --------------------------------------------------------- whole layers ----
+
+// T into the workspace; with an 8-bit base (`q`) X's codes and scales too.
+lora_status_t launch_t_codes(const void* X, const void* A, int64_t M, int64_t d_in, int32_t r, float scale,
+                             const DropArgs& drop, __nv_bfloat16* Tws, const Rounded* q, int sm_count,
+                             cudaStream_t st) {
+  if (q != nullptr && use_prep(M, r, drop)) return launch_prep(X, A, M, d_in, r, scale, Tws, *q, st);
+  return launch_down(X, A, M, d_in, r, scale, drop, Tws, q, sm_count, st);
+}
+
+// Where a call's intermediate values lie in its workspace.
+struct Places {
+  __nv_bfloat16 *T, *dT;
+  Rounded q;  // (8-bit base)
+  Places(void* workspace, int64_t M, int64_t d_in, int64_t d_out, int32_t r) {
+    uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
+    const BwdWorkspace w = bwd_workspace(M, r);
+    const Fp8Workspace f = fp8_workspace(M, d_in, d_out, r);
+    T = reinterpret_cast<__nv_bfloat16*>(ws + w.off_t);
+    dT = reinterpret_cast<__nv_bfloat16*>(ws + w.off_dt);
+    q = Rounded{ws + f.off_codes, ws + f.off_scales, ScaleAtomArgs{}};
+    q.atoms.atoms = ws + f.off_atoms;
+  }
+};
 
 // Forward.  Arguments already validated.
 lora_status_t adapter_fwd_run(const void* X, const Base& W, const void* A, const void* B, void* Y, int64_t M,
@@ -289,17 +403,20 @@ lora_status_t adapter_fwd_run(const void* X, const Base& W, const void* A, const
   DeviceInfo dev;
   lora_status_t s = device_info(dev);
   if (s != LORA_OK || M == 0) return s;
-  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
-  __nv_bfloat16* const Tws = reinterpret_cast<__nv_bfloat16*>(ws + bwd_workspace(M, r).off_t);
-  const Fp8Workspace q = fp8_workspace(M, d_in, d_out, r);
-  uint8_t* const codes = W.fp8() ? ws + q.off_codes : nullptr;
-  uint8_t* const scales = W.fp8() ? ws + q.off_scales : nullptr;
-  if ((s = launch_down(X, A, M, d_in, r, scale, drop, Tws, codes, scales, dev.sm_count, st)) != LORA_OK) return s;
-  return launch_up(W.fp8() ? codes : X, scales, W, B, Y, Tws, M, d_in, d_out, r, dev.sm_count, st);
+  const int sms = dev.sm_count;
+  const bool fp8 = W.fp8(), stream = fp8 && M <= kStreamMax;
+  Places at(workspace, M, d_in, d_out, r);
+  LrCfg c;
+  if (!stream) pick_lr(M, d_out, d_in, r, fp8, false, sms, c);
+  if (fp8 && !stream) at.q.atoms = scale_atom_args(W, at.q, c, false, d_in, d_out);
+  if ((s = launch_t_codes(X, A, M, d_in, r, scale, drop, at.T, fp8 ? &at.q : nullptr, sms, st)) != LORA_OK) return s;
+  if (stream) return launch_stream(W, B, Y, M, d_in, d_out, r, at.T, at.q.codes, at.q.scales, sms, st);
+  c.args.f.out = reinterpret_cast<__nv_bfloat16*>(Y);
+  return launch_up(X, at.q, W, B, Y, at.T, c, r, sms, st);
 }
 
 // Backward.  Arguments already validated.
-//  1. dT = s dY B (with an 8-bit base also dY's codes), and T unless saved;
+//  1. T unless saved, and dT = s dY B (with an 8-bit base also dY's codes);
 //  2. dB = dY^T T and dA = dT^T (m * X)/(1-p), one launch;
 //  3. dX.
 lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const void* B, const void* dY, void* dX,
@@ -317,30 +434,34 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
     return zero_bytes(dB, size_t(d_out) * size_t(r) * gb, st);
   }
   const int sms = dev.sm_count;
-  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
-  const BwdWorkspace w = bwd_workspace(M, r);
-  const Fp8Workspace q = fp8_workspace(M, d_in, d_out, r);
-  __nv_bfloat16* const Tws = reinterpret_cast<__nv_bfloat16*>(ws + w.off_t);
-  __nv_bfloat16* const dTws = reinterpret_cast<__nv_bfloat16*>(ws + w.off_dt);
-  uint8_t* const codes = fp8 ? ws + q.off_codes : nullptr;
-  uint8_t* const scales = fp8 ? ws + q.off_scales : nullptr;
+  Places at(workspace, M, d_in, d_out, r);
   const int r_pad = r_pad_of(r);
   const int rcw = rcw_of(r_pad);
 
+  // (X's codes are not needed here, but this way T is the forward's bit for bit)
   if (!saved &&
-      (s = launch_down(X, A, M, d_in, r, scale, drop, Tws, nullptr, nullptr, sms, st)) != LORA_OK)
+      (s = launch_t_codes(X, A, M, d_in, r, scale, drop, at.T, fp8 ? &at.q : nullptr, sms, st)) != LORA_OK)
     return s;
+  LrCfg c;
+  pick_lr(M, d_in, d_out, r, fp8, true, sms, c);
+  c.args.f.out = reinterpret_cast<__nv_bfloat16*>(dX);
+  c.args.drop = drop;
   {
-    PassCfg c;
-    pick_pass(M, d_out, r, false, true, OUT_ROWS_RPAD, (M + 127) / 128, sms, c);
-    c.args.out = dTws;
-    c.args.scale = scale;
-    c.args.codes = codes;
-    c.args.scales = scales;
+    PassCfg p;
+    pick_pass(M, d_out, r, false, true, OUT_ROWS_RPAD, (M + 127) / 128, sms, p);
+    p.args.out = at.dT;
+    p.args.scale = scale;
     PassMaps m;
     if (!make_map(&m.p, dY, d_out, M, d_out, 64, 128, 128) || !make_map(&m.r, B, r, d_out, r, rcw, 64, rcw * 2))
       return LORA_ERR_CUDA;
-    s = fp8 ? launch_pass<false, true>(m, c, st) : launch_pass<false, false>(m, c, st);
+    if (fp8) {
+      p.args.codes = at.q.codes;
+      p.args.scales = at.q.scales;
+      at.q.atoms = scale_atom_args(W, at.q, c, true, d_in, d_out);
+      s = launch_pass<false, true>(m, p, st, nullptr, nullptr, at.q.atoms);
+    } else {
+      s = launch_pass<false, false>(m, p, st);
+    }
     if (s != LORA_OK) return s;
   }
   {
@@ -357,13 +478,13 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
     ca.args.drop = drop;
     PassMaps mb, ma;
     if (!make_map(&mb.p, dY, d_out, M, d_out, 64, 64, 128) ||
-        !make_map(&mb.r, Tws, r_pad, M, r_pad, rcw, 64, rcw * 2) ||
+        !make_map(&mb.r, at.T, r_pad, M, r_pad, rcw, 64, rcw * 2) ||
         !make_map(&ma.p, X, d_in, M, d_in, 64, 64, 128) ||
-        !make_map(&ma.r, dTws, r_pad, M, r_pad, rcw, 64, rcw * 2))
+        !make_map(&ma.r, at.dT, r_pad, M, r_pad, rcw, 64, rcw * 2))
       return LORA_ERR_CUDA;
     if ((s = launch_pass<true, false>(mb, cb, st, &ma, &ca)) != LORA_OK) return s;
   }
-  return launch_dx(fp8 ? codes : dY, scales, W, A, dX, dTws, M, d_in, d_out, r, drop, sms, st);
+  return launch_dx(dY, at.q, W, A, dX, at.dT, c, r, sms, st);
 }
 
 // Pointer and workspace rules of the four layer entry points (sizes already

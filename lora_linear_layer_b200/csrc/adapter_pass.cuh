@@ -48,7 +48,7 @@ struct PassArgs {
   __nv_bfloat16* out;     // (a float* when out_f32)
   DropArgs drop;          // rng NULL: P is used as it is
   uint8_t* codes;         // QUANT: [rows, K] e4m3
-  uint8_t* scales;        // QUANT: e8m0 bytes, [ceil(K / 512)][rows][4]
+  uint8_t* scales;        // QUANT: e8m0 bytes (scale_atom_offset)
   uint64_t wait_limit_ns;
 };
 
@@ -68,12 +68,22 @@ struct PassLayout {
 };
 
 template <bool P_MN, int RCW, bool QUANT>
-__global__ void __launch_bounds__(kPassThreads)
+__global__ void __launch_bounds__(kPassThreads, 2)
     adapter_pass_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmR0,
                         const __grid_constant__ CUtensorMap tmP1, const __grid_constant__ CUtensorMap tmR1,
                         const __grid_constant__ PassArgs a0, const __grid_constant__ PassArgs a1,
-                        const int32_t x_split) {
+                        const int32_t x_split, const int32_t x_atoms, const __grid_constant__ ScaleAtomArgs atoms) {
   static_assert(!(P_MN && QUANT), "codes are written row by row");
+  if constexpr (QUANT) {
+    if (int(blockIdx.x) >= x_atoms) {  // blocks behind the row tiles: the other operand's scales
+      griddep_wait();
+      griddep_launch_dependents();
+      const int blocks = int(gridDim.x) - x_atoms, block = int(blockIdx.x) - x_atoms + blocks * int(blockIdx.y);
+      scale_atoms(atoms, block * (kPassThreads / 32) + int(threadIdx.x >> 5),
+                  blocks * int(gridDim.y) * (kPassThreads / 32), int(threadIdx.x & 31u));
+      return;
+    }
+  }
   const bool second = int(blockIdx.x) >= x_split;
   const PassArgs& a = second ? a1 : a0;
   const int bx = second ? int(blockIdx.x) - x_split : int(blockIdx.x);
@@ -211,59 +221,69 @@ __global__ void __launch_bounds__(kPassThreads)
     int stage = 0;
     uint32_t phase = 0;
     const int c = lane & 7, r4 = lane >> 3;
+    // Addresses inside a stage: a lane's 16-byte chunk of rows w * kRows + r4
+    // and four rows on (the swizzle repeats every 8 rows).
+    //  K-major: four rows at a time, 8 lanes a row, 16 consecutive values a
+    //  lane: sub-stage c / 4, chunks 2 (c % 4) and the next.  The lanes of
+    //  the second sub-stage take theirs in the other order, so that the 8
+    //  lanes of a row touch 8 different bank groups.
+    //  MN-major: 128 (column chunk of 64, token) rows, 8 lanes a row.
+    constexpr int kRows = 128 / kPassWorkers;
+    const uint32_t odd = P_MN ? 0u : uint32_t(c >> 2);
+    uint32_t off[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t row = uint32_t(w * kRows + 4 * i + r4);
+      off[i] = P_MN ? (row >> 6) * 8192u + swz_offset(row & 63u, uint32_t(c), 128u)
+                    : odd * L.sub_bytes + swz_offset(row, uint32_t(c & 3) * 2u + odd, 128u);
+    }
+    const int row0 = P_MN ? (w * kRows + r4) & 63 : i0 + w * kRows + r4;  // token in the stage, or row of P
+    const uint32_t c8_mn = uint32_t(i0 + (w * kRows >> 6) * 64) / 8u + uint32_t(c);
+    const bool any = P_MN || i0 + w * kRows < a.rows;  // (rows past the end are zero fill)
+    const int row_blocks = (a.rows + 127) / 128;
+    const size_t code0 = size_t(row0) * size_t(a.K) + size_t(c * 16);
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!warp_wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL)) break;
       const uint32_t st = sbase + uint32_t(stage) * L.stage_bytes;
       if constexpr (!P_MN) {
-        // Four rows at a time, 8 lanes a row, 16 consecutive values a lane:
-        // sub-stage c / 4, chunks 2 (c % 4) and the next.  The lanes of the
-        // second sub-stage take theirs in the other order, so that the 8
-        // lanes of a row touch 8 different bank groups.
-        const int sub = c >> 2, odd = sub;
-        const uint32_t ps = st + uint32_t(sub) * L.sub_bytes;
-        const int k = kb * 128 + c * 16;
-#pragma unroll 2
-        for (int it = 0; it < 4; ++it) {
-          const int row = w * 16 + it * 4 + r4;
-          const int gi = i0 + row;
-          if (i0 + w * 16 + it * 4 >= a.rows) break;  // rows past the end are zero fill (the whole warp agrees)
-          const uint32_t cp = uint32_t(c & 3) * 2u;
-          const uint32_t a_first = ps + swz_offset(uint32_t(row), cp + odd, 128u);
-          const uint32_t a_second = ps + swz_offset(uint32_t(row), cp + (odd ^ 1), 128u);
-          const uint4 v_first = ld_shared_v4(a_first), v_second = ld_shared_v4(a_second);
-          const uint4 lo = odd ? v_second : v_first, hi = odd ? v_first : v_second;
-          if constexpr (QUANT) {
-            uint32_t m = amax_bf16x8(amax_bf16x8(0u, lo), hi);
+        if (any) {
+          const int k = kb * 128 + c * 16;
 #pragma unroll
-            for (int s = 4; s > 0; s >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, s));
-            const uint32_t b = e8m0_of_amax(max(m & 0xFFFFu, m >> 16));
-            const uint4 q = quant16(lo, hi, e8m0_inverse(b));
-            if (gi < a.rows) {
-              if (k < a.K) *reinterpret_cast<uint4*>(a.codes + size_t(gi) * size_t(a.K) + size_t(k)) = q;
-              if (c == 0) a.scales[(size_t(kb >> 2) * size_t(a.rows) + size_t(gi)) * 4 + size_t(kb & 3)] = uint8_t(b);
+          for (int it = 0; it < kRows / 4; ++it) {
+            // chunk 2 (c % 4) + odd, and the other of the two
+            const uint32_t at0 = st + off[it & 1] + uint32_t(it >> 1) * 1024u, at1 = at0 ^ 16u;
+            const uint4 v0 = ld_shared_v4(at0), v1 = ld_shared_v4(at1);
+            const int gi = row0 + 4 * it;
+            if constexpr (QUANT) {
+              uint32_t m = amax_bf16x16(v0, v1);
+#pragma unroll
+              for (int s = 4; s > 0; s >>= 1) m = amax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, s));
+              const uint32_t b = e8m0_of_pair(m), f = e8m0_inverse(b);
+              const uint2 q0 = quant8(v0, f), q1 = quant8(v1, f);
+              if (gi < a.rows) {
+                if (k < a.K)
+                  *reinterpret_cast<uint4*>(a.codes + code0 + size_t(4 * it) * size_t(a.K) + size_t(kb) * 128) =
+                      odd ? make_uint4(q1.x, q1.y, q0.x, q0.y) : make_uint4(q0.x, q0.y, q1.x, q1.y);
+                if (c == 0)
+                  a.scales[scale_atom_offset(gi, kb, row_blocks)] = uint8_t(b);
+              }
             }
-          }
-          if (drop) {
-            const uint32_t c8 = uint32_t(k) >> 3;
-            const uint4 dlo = drop_bf16x8(lo, drop_block(ds, c8, uint32_t(gi)), ds.thr_hi);
-            const uint4 dhi = drop_bf16x8(hi, drop_block(ds, c8 + 1u, uint32_t(gi)), ds.thr_hi);
-            st_shared_v4(a_first, odd ? dhi : dlo);
-            st_shared_v4(a_second, odd ? dlo : dhi);
+            if (drop) {
+              const uint32_t c8 = uint32_t(k) >> 3;
+              st_shared_v4(at0, drop_bf16x8(v0, drop_block(ds, c8 + odd, uint32_t(gi)), ds.thr_hi));
+              st_shared_v4(at1, drop_bf16x8(v1, drop_block(ds, c8 + (odd ^ 1u), uint32_t(gi)), ds.thr_hi));
+            }
           }
         }
       } else {
-        // 64 rows of the contraction (tokens) x two chunks of 64 columns
-#pragma unroll 2
-        for (int it = 0; it < 4; ++it) {
-          const int unit = w * 16 + it * 4 + r4;  // 128 (column chunk, token) rows
-          const int cc = unit >> 6, tok = unit & 63;
-          const uint32_t addr = st + uint32_t(cc) * 8192u + swz_offset(uint32_t(tok), uint32_t(c), 128u);
-          const uint32_t c8 = uint32_t(i0 + cc * 64) / 8u + uint32_t(c);
-          const uint4 v = ld_shared_v4(addr);
-          st_shared_v4(addr, drop_bf16x8(v, drop_block(ds, c8, uint32_t(kb * 64 + tok)), ds.thr_hi));
+#pragma unroll
+        for (int it = 0; it < kRows / 4; ++it) {
+          const uint32_t addr = st + off[it & 1] + uint32_t(it >> 1) * 1024u;
+          const uint32_t tok = uint32_t(kb * 64 + row0 + 4 * it);
+          st_shared_v4(addr, drop_bf16x8(ld_shared_v4(addr), drop_block(ds, c8_mn, tok), ds.thr_hi));
         }
       }
-      fence_proxy_async_smem();
+      if (drop) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(ready_bar(stage));
       if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -281,7 +301,7 @@ __global__ void __launch_bounds__(kPassThreads)
     if (have) {
       const int q = warp & 3;
       const uint32_t lane_base = uint32_t(q * 32) << 16;
-      for (int col = 16 * ((warp - 2) >> 2); col < a.r_pad; col += 32) {
+      for (int col = 16 * ((warp - 2) >> 2); col < a.r_pad; col += 4 * kPassWorkers) {
         uint32_t v[16];
         if (nkb > 0) {
           tmem_ld_x16(tmem + lane_base + uint32_t(col), v);

@@ -22,33 +22,51 @@ namespace lora {
 
 constexpr int kQBlock = 128;
 
-// |x| of two packed bf16, as integers that order like the magnitudes
-// (infinities and NaN above every finite value).
+// Largest magnitudes of packed bf16 pairs; a NaN wins.  The result's sign is
+// the xor of the operands' (the form that needs no separate absolute values);
+// abs_bf16x2 clears it at the end.
+__device__ __forceinline__ uint32_t amax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t abs_bf16x2(uint32_t v) { return v & 0x7FFF7FFFu; }
 
-__device__ __forceinline__ uint32_t amax_bf16x8(uint32_t m, uint4 v) {
-  m = __vmaxu2(m, abs_bf16x2(v.x));
-  m = __vmaxu2(m, abs_bf16x2(v.y));
-  m = __vmaxu2(m, abs_bf16x2(v.z));
-  return __vmaxu2(m, abs_bf16x2(v.w));
+__device__ __forceinline__ uint32_t amax_bf16x16(uint4 x, uint4 y) {
+  return amax_bf16x2(amax_bf16x2(amax_bf16x2(x.x, x.y), amax_bf16x2(x.z, x.w)),
+                     amax_bf16x2(amax_bf16x2(y.x, y.y), amax_bf16x2(y.z, y.w)));
 }
 
 // The e8m0 byte of a group whose largest magnitude has these bf16 bits.
 // amax = 1.f * 2^x fits under 448 * 2^e = 1.75 * 2^(e + 8) with e = x - 8
-// when its fraction is at most .75 (96 of 128), else with e = x - 7.  A
-// subnormal bf16 (x < -126) is below 448 * 2^-127 in any case.
+// when its fraction is at most .75 (96 of 128), else with e = x - 7: adding
+// 31 carries exactly then.  A subnormal bf16 (x < -126) is below
+// 448 * 2^-127 in any case.
 __device__ __forceinline__ uint32_t e8m0_of_amax(uint32_t amax_bits) {
   if (amax_bits >= 0x7F80u) return 255u;
   if (amax_bits == 0u) return 127u;
-  const int biased = int(amax_bits >> 7);
-  const int b = biased - ((amax_bits & 0x7Fu) <= 96u ? 8 : 7);
-  return b > 0 ? uint32_t(b) : 0u;
+  return uint32_t(max(int((amax_bits + 31u) >> 7) - 8, 0));
 }
 
-// 2^-(b - 127), the factor that a value is multiplied by (exact: b is at
-// most 247; 1 for the NaN scale).
-__device__ __forceinline__ float e8m0_inverse(uint32_t b) {
-  return b == 255u ? 1.0f : __uint_as_float((254u - b) << 23);
+// The same for the larger of two packed magnitudes (signs are ignored).
+__device__ __forceinline__ uint32_t e8m0_of_pair(uint32_t m) {
+  m = abs_bf16x2(m);
+  return e8m0_of_amax(max(m & 0xFFFFu, m >> 16));
+}
+
+// 2^-(b - 127) as two packed bf16, the factor that values are multiplied by
+// (b is at most 247; 1 for the NaN scale).  The product of a bf16 value is
+// exact in bf16, except far below the smallest e4m3 value, where the code is
+// zero in any case.
+__device__ __forceinline__ uint32_t e8m0_inverse(uint32_t b) {
+  return b == 255u ? 0x3F803F80u : ((254u - b) << 7) * 0x10001u;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ float e8m0_value(uint32_t b) {
@@ -63,15 +81,18 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Four bf16 (two words) times `f` -> four codes.
-__device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, float f) {
-  const uint32_t lo = pack_e4m3x2(bf16lo_to_f32(a) * f, bf16hi_to_f32(a) * f);
-  const uint32_t hi = pack_e4m3x2(bf16lo_to_f32(b) * f, bf16hi_to_f32(b) * f);
+// Four scaled bf16 (two words) -> four codes.
+__device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, uint32_t f) {
+  a = mul_bf16x2(a, f);
+  b = mul_bf16x2(b, f);
+  const uint32_t lo = pack_e4m3x2(bf16lo_to_f32(a), bf16hi_to_f32(a));
+  const uint32_t hi = pack_e4m3x2(bf16lo_to_f32(b), bf16hi_to_f32(b));
   return lo | (hi << 16);
 }
 
-__device__ __forceinline__ uint4 quant16(uint4 a, uint4 b, float f) {
-  return make_uint4(quant4(a.x, a.y, f), quant4(a.z, a.w, f), quant4(b.x, b.y, f), quant4(b.z, b.w, f));
+// 8 consecutive bf16 with the scale's inverse -> 8 codes.
+__device__ __forceinline__ uint2 quant8(uint4 x, uint32_t f) {
+  return make_uint2(quant4(x.x, x.y, f), quant4(x.z, x.w, f));
 }
 
 // Two e4m3 codes (low 16 bits) -> two fp32 (through fp16, which holds every
@@ -84,6 +105,50 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t v) {
       : "=f"(f.x), "=f"(f.y)
       : "r"(h));
   return f;
+}
+
+// ---------------------------------------------------- scales of a product ----
+//
+// tcgen05.mma reads its scales from TMEM as 32 lanes x 4 columns of 32-bit
+// words for 128 rows (columns) of a tile: row r is lane r % 32, column r / 32,
+// and the four bytes of a word are the scales of four consecutive blocks of
+// 128 values of K.  One such "atom" is 512 bytes, 16 a lane.
+//   rows of X or dY:    [ceil(K / 512)][ceil(M / 128)] atoms, written by the
+//                       pass that rounds them;
+//   columns of a tile:  [tile][ceil(K / 512)][2] atoms for the tile's up to
+//                       256 columns, laid out from the weight's bytes for
+//                       each call (scale_atoms) since a tile's columns need
+//                       not begin on a block of 128.
+
+// Byte offset of the scale of (row, block kb of K), `blocks` = ceil(M / 128).
+__device__ __forceinline__ size_t scale_atom_offset(int row, int kb, int blocks) {
+  return (size_t(kb >> 2) * size_t(blocks) + size_t(row >> 7)) * 512 +
+         size_t((row & 31) * 16 + ((row >> 5) & 3) * 4 + (kb & 3));
+}
+
+struct ScaleAtomArgs {
+  const uint8_t* bytes;   // the weight's scales, or NULL: no atoms to lay out
+  uint8_t* atoms;         // [tiles][groups][2][512]
+  int32_t tiles, groups;  // of the product
+  int32_t bn;             // columns of a tile
+  int32_t n_blocks, k_blocks, ld_n, ld_k;  // of `bytes`, along the product's N and K
+};
+
+// One warp's share of the column atoms: every `step`-th atom from `item` on.
+__device__ __forceinline__ void scale_atoms(const ScaleAtomArgs& a, int item, int step, int lane) {
+  for (; item < a.tiles * a.groups * 2; item += step) {
+    const int tile = item / (2 * a.groups), g = (item >> 1) % a.groups, half = item & 1;
+    // byte lane & 3 of word (lane >> 2) & 3
+    const int n = tile * a.bn + 128 * half + 32 * ((lane >> 2) & 3);
+    const int nb = imin(n >> 7, a.n_blocks - 1), kb = imin(4 * g + (lane & 3), a.k_blocks - 1);
+    uint32_t v = uint32_t(a.bytes[size_t(nb) * size_t(a.ld_n) + size_t(kb) * size_t(a.ld_k)]) << (8 * (lane & 3));
+    v |= __shfl_xor_sync(0xffffffffu, v, 1);
+    v |= __shfl_xor_sync(0xffffffffu, v, 2);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(0xffffffffu, v, 4 * i);
+    reinterpret_cast<uint4*>(a.atoms)[size_t(item) * 32 + size_t(lane)] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 constexpr int kQuantThreads = 256;
@@ -101,7 +166,6 @@ __global__ void __launch_bounds__(kQuantThreads)
   const int col = cb * kQBlock + int(threadIdx.x & 7u) * 16;
   const int row0 = rb * kQBlock + int(threadIdx.x >> 3);
   uint4 v[4][2];
-  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + 32 * i;
@@ -110,22 +174,24 @@ __global__ void __launch_bounds__(kQuantThreads)
     v[i][0] = in ? __ldcs(src) : make_uint4(0, 0, 0, 0);
     v[i][1] = in ? __ldcs(src + 1) : make_uint4(0, 0, 0, 0);
   }
+  uint32_t m = amax_bf16x16(v[0][0], v[0][1]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = amax_bf16x8(amax_bf16x8(m, v[i][0]), v[i][1]);
+  for (int i = 1; i < 4; ++i) m = amax_bf16x2(m, amax_bf16x16(v[i][0], v[i][1]));
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, s));
+  for (int s = 16; s > 0; s >>= 1) m = amax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, s));
   if ((threadIdx.x & 31u) == 0u) warp_max[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kQuantThreads / 32; ++i) m = __vmaxu2(m, warp_max[i]);
-  const uint32_t b = e8m0_of_amax(max(m & 0xFFFFu, m >> 16));
-  const float f = e8m0_inverse(b);
+  for (int i = 0; i < kQuantThreads / 32; ++i) m = amax_bf16x2(m, warp_max[i]);
+  const uint32_t b = e8m0_of_pair(m);
+  const uint32_t f = e8m0_inverse(b);
   if (threadIdx.x == 0) Ws[blockIdx.x] = uint8_t(b);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + 32 * i;
+    const uint2 lo = quant8(v[i][0], f), hi = quant8(v[i][1], f);
     if (row < rows && col < cols)
-      *reinterpret_cast<uint4*>(Wq + size_t(row) * size_t(cols) + size_t(col)) = quant16(v[i][0], v[i][1], f);
+      *reinterpret_cast<uint4*>(Wq + size_t(row) * size_t(cols) + size_t(col)) = make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
 }
 

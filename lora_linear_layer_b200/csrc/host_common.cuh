@@ -106,7 +106,8 @@ lora_status_t device_info(DeviceInfo& out) {
 }
 
 CUtensorMapSwizzle swz_enum(uint32_t span_bytes) {
-  return span_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+  return span_bytes == 0 ? CU_TENSOR_MAP_SWIZZLE_NONE
+         : span_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
          : span_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                             : CU_TENSOR_MAP_SWIZZLE_32B;
 }
@@ -137,8 +138,8 @@ struct MapKeyHash {
 constexpr size_t kMapCache = 8192;
 thread_local std::unordered_map<MapKey, CUtensorMap, MapKeyHash> t_maps;
 
-// (`bytes` = bytes per element: 2 = bf16, 1 = raw bytes; in the key beside
-// the swizzle span, which is at most 128.)
+// (`bytes` = bytes per element: 2 = bf16, 1 and 4 = raw; in the key beside the
+// swizzle span, which is at most 128; 0 = no swizzle.)
 bool make_map_sized(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
                     uint32_t box_outer, uint32_t swz_span_bytes, uint32_t bytes) {
   const MapKey k{ptr, inner, outer, ld, box_inner, box_outer, swz_span_bytes | bytes << 16};
@@ -151,7 +152,9 @@ bool make_map_sized(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t ou
   cuuint64_t strides[1] = {ld * bytes};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType type = bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapDataType type = bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32
+                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUresult rc = g_encode(m, type, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                                CU_TENSOR_MAP_INTERLEAVE_NONE, swz_enum(swz_span_bytes),
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -174,6 +177,11 @@ bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, u
 bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
                  uint32_t box_outer) {
   return make_map_sized(m, ptr, inner, outer, ld, box_inner, box_outer, 128, 1);
+}
+
+// `n` scale atoms of 512 bytes (fp8.cuh), `box` at a time.
+bool make_map_atoms(CUtensorMap* m, const void* ptr, uint64_t n, uint32_t box) {
+  return make_map_sized(m, ptr, 128, n, 128, 128, box, 0, 4);
 }
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel, device

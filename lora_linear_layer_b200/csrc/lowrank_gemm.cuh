@@ -18,15 +18,21 @@
 // (128-byte rows, as 64 bf16 are), so the ring, the swizzle and the
 // descriptors are those of the bf16 form.  The scales of four stages are the
 // four bytes of one 32-bit word for each row (column) of the tile, selected
-// by the scale index of the instruction descriptor: one warp builds the
-// words of a tile's 128 rows and BN columns in shared memory every four
-// stages and the MMA thread copies them to TMEM (tcgen05.cp).  Two
-// accumulators of 224 columns leave 64 columns of TMEM for them: four
-// buffers of 16 columns, and a buffer comes round again after 16 stages,
-// more than the ring has, so the MMAs that read it are done.
+// by the scale index of the instruction descriptor.  They lie in memory as
+// the tensor core reads them (scale_atom_offset) and come with the first of
+// the four stages, by TMA and on its barrier; the MMA thread copies them to
+// TMEM (tcgen05.cp) and does nothing else for them: its own instructions are
+// what keeps the tensor pipe waiting at 8 bits.  (A warp that built the words
+// in shared memory cost a wait and a commit there: 123 us against 109 us on
+// 8192 x 4096 x 4096.)  Two accumulators of 224 columns leave 64 columns of
+// TMEM for scales: four buffers of 16 columns.  A buffer comes round again
+// after four groups of stages, which are seven stages or more (a group is one
+// stage only where K <= 128, and then each but the last tile's has a rank
+// block before it); the ring has at most seven, so the MMAs that read a buffer
+// are done when the stage that brings its next scales can be filled.
 //
-// Tiles are CTA pairs (cta_group::2) of 256 x BN, walked in the order of
-// fused.cuh's dX form.  What bounds it is the tensor pipe.
+// Tiles are CTA pairs (cta_group::2) of 256 x BN.  What bounds it is the
+// tensor pipe.
 #pragma once
 
 #include "common.cuh"
@@ -36,15 +42,33 @@
 namespace lora {
 
 constexpr int kLrScaleBufs = 4;
+constexpr int kLrMaxStagesFp8 = 7;
 constexpr uint32_t kLrScaleBytes = 512u * 3u;  // A: 128 rows, B: 256 columns, 4 bytes each
 
 struct LrArgs {
-  FusedArgs f;               // sizes, tile counts, schedule, stages, ep_bufs
+  FusedArgs f;               // sizes, tile counts, stages, ep_bufs
+  int32_t group_m;           // M blocks walked together (LrSched)
   DropArgs drop;             // DROP: the mask of OUT's [M, N]
-  const uint32_t* p_scales;  // FP8: words of 4 scale bytes, [ceil(K / 512)][M]
-  const uint8_t* q_scales;   // FP8: bytes of 128 x 128 blocks
-  int32_t qs_n, qs_k;        // their counts along N and K
-  int32_t qs_ld_n, qs_ld_k;  // and strides
+};
+
+// Tiles are dealt one at a time, group by group of `group_m` M blocks and M
+// fastest inside a group: the tiles in flight share their rows of P, which
+// stay in L2 for the whole group, and the same few columns of Q, so Q is read
+// from memory once a group.
+struct LrSched {
+  int num_m, num_n, group_m, G, t;
+  __device__ LrSched(const LrArgs& a, int G_, int c)
+      : num_m(a.f.num_m), num_n(a.f.num_n), group_m(a.group_m), G(G_), t(c) {}
+  __device__ bool next(int& m, int& n) {
+    if (t >= num_m * num_n) return false;
+    const int per = group_m * num_n;
+    const int g = t / per, i = t - g * per;
+    const int w = imin(group_m, num_m - g * group_m);
+    n = i / w;
+    m = g * group_m + (i - n * w);
+    t += G;
+    return true;
+  }
 };
 
 template <bool FP8, bool MN, int BN>
@@ -55,7 +79,6 @@ struct LrShape {
   static constexpr uint32_t kQRank = !MN ? kBNC * 128u : kChunks * 8192u;                 // bytes loaded, rank block
   static constexpr uint32_t kQSlot = kQBase > kQRank ? kQBase : kQRank;
   static constexpr uint32_t kStage = 16384u + kQSlot;
-  static constexpr int kThreads = FP8 ? kFusedThreads + 32 : kFusedThreads;
 };
 
 struct LrLayout {
@@ -69,10 +92,11 @@ struct LrLayout {
 };
 
 template <bool FP8, bool MN, bool DROP, int BN>
-__global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
+__global__ void __launch_bounds__(kFusedThreads, 1)
     lowrank_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmV,
-                        const __grid_constant__ CUtensorMap tmO, const __grid_constant__ LrArgs la) {
+                        const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmPS,
+                        const __grid_constant__ CUtensorMap tmQS, const __grid_constant__ LrArgs la) {
   static_assert(BN % 32 == 0 && 2 * BN + (FP8 ? 16 * kLrScaleBufs : 0) <= 512, "TMEM");
   static_assert(!DROP || MN, "only dX masks its rank product");
   using Sh = LrShape<FP8, MN, BN>;
@@ -88,7 +112,7 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
   const LrLayout L(Sh::kStage, FP8, a.stages, a.ep_bufs);
   const int S = a.stages;
   const uint32_t bar0 = sbase + L.off_bar;
-  // full, accempty, masked, sffull and drain are used on the even CTA only
+  // full, accempty, masked and drain are used on the even CTA only
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
   const uint32_t accfull0 = bar0 + 8u * (2 * S);        // +8*b
@@ -96,10 +120,7 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
   const uint32_t rankfull = bar0 + 8u * (2 * S + 4);    // DROP: a rank product is in its accumulator
   const uint32_t masked = bar0 + 8u * (2 * S + 5);      // DROP: ... and masked
   const uint32_t drain = bar0 + 8u * (2 * S + 6);
-  const uint32_t sffull0 = bar0 + 8u * (2 * S + 7);     // +8*buf
-  const uint32_t sfempty0 = sffull0 + 8u * kLrScaleBufs;
-  uint32_t* const tmem_slot =
-      reinterpret_cast<uint32_t*>(gbase + L.off_bar + 8 * (2 * S + 7 + 2 * kLrScaleBufs));
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + L.off_bar + 8 * (2 * S + 7));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -119,10 +140,6 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
     mbar_init(rankfull, 1);
     mbar_init(masked, 8);
     mbar_init(drain, 1);
-    for (int i = 0; i < kLrScaleBufs; ++i) {
-      mbar_init(sffull0 + 8u * i, 2);
-      mbar_init(sfempty0 + 8u * i, 1);
-    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -131,6 +148,10 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmU);
     tma_prefetch_desc(&tmV);
+    if constexpr (FP8) {
+      tma_prefetch_desc(&tmPS);
+      tma_prefetch_desc(&tmQS);
+    }
   }
   if (warp == 2 && lane == 0) tma_prefetch_desc(&tmO);
   if (warp == 1) G::alloc(smem_addr(tmem_slot), 512);
@@ -153,14 +174,16 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------ TMA producer ----
     if (lane == 0) {
-      TileSched sch(a, n_clusters, cluster_id);
+      LrSched sch(la, n_clusters, cluster_id);
       int stage = 0;
       uint32_t phase = 0;
+      uint32_t sf_n = 0;                      // scale groups so far
+      const int groups = (nk + 3) / 4, p_blocks = (a.M + 127) / 128;
       auto claim = [&](uint32_t bytes, uint32_t& st, uint32_t& fb) -> bool {
         if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, lim, SITE_EMPTY, true)) return false;
         st = sbase + uint32_t(stage) * Sh::kStage;
         fb = G::leader_addr(full_bar(stage));
-        if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * (16384u + bytes));
+        if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
         if (++stage == S) { stage = 0; phase ^= 1u; }
         return true;
       };
@@ -169,7 +192,7 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
         const int q0 = n * BN + int(rank) * BNC;
         for (int rb = 0; rb < nr; ++rb) {
           uint32_t st, fb;
-          if (!claim(Sh::kQRank, st, fb)) return false;
+          if (!claim(16384u + Sh::kQRank, st, fb)) return false;
           G::load(st, &tmU, fb, rb * 64, row0);
           if constexpr (!MN) {
             G::load(st + 16384u, &tmV, fb, rb * 64, q0);
@@ -186,8 +209,16 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
         const int q0 = n * BN + int(rank) * BNC;
         for (int kb = from; kb < to; ++kb) {
           uint32_t st, fb;
-          if (!claim(Sh::kQBase, st, fb)) return false;
+          const bool scales = FP8 && (kb & 3) == 0;
+          if (!claim(16384u + Sh::kQBase + (scales ? kLrScaleBytes : 0u), st, fb)) return false;
           const int k0 = kb * kStageK;
+          if constexpr (FP8) {
+            if (scales) {
+              const uint32_t sf = sbase + L.off_sf + (sf_n++ % kLrScaleBufs) * kLrScaleBytes;
+              G::load(sf, &tmPS, fb, 0, (kb >> 2) * p_blocks + 2 * m + int(rank));
+              G::load(sf + 512u, &tmQS, fb, 0, 2 * (n * groups + (kb >> 2)));
+            }
+          }
           G::load(st, &tmP, fb, k0, row0);
           if constexpr (!MN) {
             G::load(st + 16384u, &tmQ, fb, k0, q0);
@@ -221,14 +252,23 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
     // ------------------------------------------------- MMA issuer ----
     if (lane == 0 && leader) {
       const uint32_t id_base = idesc_bf16(256, BN, false, MN);  // also the rank blocks' (V has Q's layout)
-      TileSched sch(a, n_clusters, cluster_id);
+      LrSched sch(la, n_clusters, cluster_id);
       int stage = 0;
       uint32_t phase = 0, sf_n = 0, marks = 0;
       uint32_t acc_waits[2] = {0u, 0u};
-      auto take = [&](uint32_t& st) -> bool {
+      // Descriptors of stage 0; a stage's are these plus its offset (in units
+      // of 16 bytes: the start address is the descriptor's low field).  This
+      // thread's own instructions are what keeps the tensor pipe waiting at
+      // 8 bits, so it does as little as it can.
+      const uint64_t p_desc = smem_desc(sbase, 16u, 1024u, SWZ_128B);
+      const uint64_t v_desc = MN ? smem_desc(sbase + 16384u, 8192u, 1024u, SWZ_128B)   // bf16 (rank blocks, base)
+                                 : smem_desc(sbase + 16384u, 16u, 1024u, SWZ_128B);
+      const uint64_t q_desc = MN && FP8 ? smem_desc(sbase + 16384u, 16384u, 1024u, SWZ_128B) : v_desc;
+      const uint64_t sf_desc = smem_desc(sbase + L.off_sf, 16u, 128u, SWZ_NONE);
+      auto take = [&](uint64_t& st) -> bool {
         if (!wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL, true)) return false;
         tc_fence_after();
-        st = sbase + uint32_t(stage) * Sh::kStage;
+        st = uint64_t(uint32_t(stage) * (Sh::kStage >> 4));
         return true;
       };
       auto give = [&]() {
@@ -242,15 +282,12 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + b * BN;
         for (int rb = 0; rb < nr; ++rb) {
-          uint32_t st;
+          uint64_t st;
           if (!take(st)) return false;
-          const uint32_t sq = st + 16384u;
           const int kk_n = imin(4, (a.r_pad - rb * 64) / 16);
           for (int kk = 0; kk < kk_n; ++kk)
-            G::mma(d, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
-                   MN ? smem_desc(sq + kk * 2048u, 8192u, 1024u, SWZ_128B)
-                      : smem_desc(sq + kk * 32u, 16u, 1024u, SWZ_128B),
-                   id_base, (rb | kk) != 0);
+            G::mma(d, p_desc + st + uint32_t(kk) * 2u, v_desc + st + uint32_t(kk) * (MN ? 128u : 2u), id_base,
+                   (rb | kk) != 0);
           give();
         }
         if constexpr (DROP) G::commit_all(rankfull);
@@ -261,36 +298,25 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
         uint32_t sf_tmem = 0;
         if constexpr (FP8) sf_tmem = tmem + 2 * BN + 16u * ((sf_n - 1u) % kLrScaleBufs);
         for (int kb = from; kb < to; ++kb) {
-          uint32_t st;
+          uint64_t st;
           if (!take(st)) return false;
-          const uint32_t sq = st + 16384u;
           if constexpr (FP8) {
             if ((kb & 3) == 0) {
-              const uint32_t buf = sf_n % kLrScaleBufs, par = (sf_n / kLrScaleBufs) & 1u;
-              ++sf_n;
-              if (!wait_bounded(sffull0 + 8u * buf, par, abort_flag, lim, SITE_TXMSG, true)) return false;
-              tc_fence_after();
+              const uint32_t buf = sf_n++ % kLrScaleBufs;
               sf_tmem = tmem + 2 * BN + 16u * buf;
-              const uint32_t src = sbase + L.off_sf + buf * kLrScaleBytes;
+              const uint64_t src = sf_desc + ((buf * kLrScaleBytes) >> 4);
 #pragma unroll
-              for (uint32_t i = 0; i < 3; ++i)
-                tmem_cp_scales_pair(sf_tmem + 4u * i, smem_desc(src + 512u * i, 16u, 128u, SWZ_NONE));
-              G::commit_all(sfempty0 + 8u * buf);
+              for (uint32_t i = 0; i < 3; ++i) tmem_cp_scales_pair(sf_tmem + 4u * i, src + 32u * i);
             }
             const uint32_t id = idesc_mxf8(256, BN, false, MN, uint32_t(kb & 3));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_mxf8_pair(d, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
-                             MN ? smem_desc(sq + kk * 4096u, 16384u, 1024u, SWZ_128B)
-                                : smem_desc(sq + kk * 32u, 16u, 1024u, SWZ_128B),
-                             id, sf_tmem, sf_tmem + 4u, 1u);
+            for (uint32_t kk = 0; kk < 4; ++kk)
+              umma_mxf8_pair(d, p_desc + st + kk * 2u, q_desc + st + kk * (MN ? 256u : 2u), id, sf_tmem, sf_tmem + 4u,
+                             1u);
           } else {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              G::mma(d, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
-                     MN ? smem_desc(sq + kk * 2048u, 8192u, 1024u, SWZ_128B)
-                        : smem_desc(sq + kk * 32u, 16u, 1024u, SWZ_128B),
-                     id_base, 1u);
+            for (uint32_t kk = 0; kk < 4; ++kk)
+              G::mma(d, p_desc + st + kk * 2u, v_desc + st + kk * (MN ? 128u : 2u), id_base, 1u);
           }
           give();
         }
@@ -318,11 +344,11 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
       G::commit_local(drain);
       wait_bounded(drain, 0u, abort_flag, lim, SITE_DRAIN, false);
     }
-  } else if (warp < 6) {
+  } else {
     // ---------------------------------------------------- epilogue ----
     const int q = warp & 3;            // TMEM lane quarter of this warp
     const uint32_t lane_base = uint32_t(q * 32) << 16;
-    TileSched sch(a, n_clusters, cluster_id);
+    LrSched sch(la, n_clusters, cluster_id);
     uint32_t ranks = 0, full_waits[2] = {0u, 0u};
     const uint32_t ep_off = L.off_ep + uint32_t(q * a.ep_bufs) * kEpBufBytes;
     uint32_t epc = 0;  // output blocks staged so far
@@ -418,51 +444,6 @@ __global__ void __launch_bounds__(LrShape<FP8, MN, BN>::kThreads, 1)
       have = more;
     }
     if (lane == 0) bulk_wait_group0();  // every output store has completed
-  } else if constexpr (FP8) {
-    // ------------------------------------------------ scale builder ----
-    TileSched sch(a, n_clusters, cluster_id);
-    const int groups = (nk + 3) / 4;
-    uint32_t sf_n = 0;
-    int m, n;
-    bool ok = true;
-    while (ok && sch.next(m, n)) {
-      const int row0 = m * 256 + int(rank) * kBM + lane;
-      // byte lane & 3 of column word lane >> 2
-      const int nb = imin((n * BN + 32 * (lane >> 2)) >> 7, la.qs_n - 1);
-      const uint8_t* const qs = la.q_scales + size_t(nb) * size_t(la.qs_ld_n);
-      auto fetch = [&](int g, uint32_t (&pa)[4], uint32_t& qb) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pa[i] = la.p_scales[size_t(g) * size_t(a.M) + size_t(imin(row0 + 32 * i, a.M - 1))];
-        qb = qs[size_t(imin(4 * g + (lane & 3), la.qs_k - 1)) * size_t(la.qs_ld_k)];
-      };
-      uint32_t pa[4], qb, pa_next[4] = {0, 0, 0, 0}, qb_next = 0;
-      fetch(0, pa, qb);
-      for (int g = 0; g < groups; ++g) {
-        if (g + 1 < groups) fetch(g + 1, pa_next, qb_next);
-        const uint32_t buf = sf_n % kLrScaleBufs, par = (sf_n / kLrScaleBufs) & 1u;
-        ++sf_n;
-        if (!warp_wait_bounded(sfempty0 + 8u * buf, par ^ 1u, abort_flag, lim, SITE_VEMPTY, true)) {
-          ok = false;
-          break;
-        }
-        uint32_t v = qb << (8 * (lane & 3));
-        v |= __shfl_xor_sync(0xffffffffu, v, 1);
-        v |= __shfl_xor_sync(0xffffffffu, v, 2);
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __shfl_sync(0xffffffffu, v, 4 * i);
-        const uint32_t dst = sbase + L.off_sf + buf * kLrScaleBytes + 16u * uint32_t(lane);
-        st_shared_v4(dst, make_uint4(pa[0], pa[1], pa[2], pa[3]));
-        st_shared_v4(dst + 512u, make_uint4(w[0], w[1], w[2], w[3]));
-        st_shared_v4(dst + 1024u, make_uint4(w[4], w[5], w[6], w[7]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) G::arrive_leader(sffull0 + 8u * buf);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pa[i] = pa_next[i];
-        qb = qb_next;
-      }
-    }
   }
 
   tc_fence_before();

@@ -23,36 +23,47 @@ struct DropArgs {
   float inv_keep;       // 65536 / (65536 - thr)
 };
 
+// The generator's constants of one call: the round keys (kept in registers;
+// stepping them in every block costs two additions a round) and the first
+// round's product of the offset word.
 struct DropState {
-  uint32_t k0, k1, o0, o1;
+  uint32_t k0[7], k1[7];
+  uint32_t o_hi, o_lo;  // words of offset low * 0xCD9E8D57
+  uint32_t o1;
   uint32_t thr_hi;      // thr << 16
 };
 
 // Reads the seed and offset (after the kernel's dependency wait).
 __device__ __forceinline__ DropState drop_load(const DropArgs& d) {
   const uint64_t seed = d.rng[0], off = d.rng[1];
-  return DropState{uint32_t(seed), uint32_t(seed >> 32), uint32_t(off), uint32_t(off >> 32), d.thr << 16};
-}
-
-__device__ __forceinline__ uint4 philox4x32_7(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
-                                              uint32_t k1) {
+  DropState s;
 #pragma unroll
-  for (int i = 0; i < 7; ++i) {
-    const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
-    const uint32_t n0 = uint32_t(b >> 32) ^ c1 ^ k0, n2 = uint32_t(a >> 32) ^ c3 ^ k1;
-    c1 = uint32_t(b);
-    c3 = uint32_t(a);
-    c0 = n0;
-    c2 = n2;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+  for (uint32_t i = 0; i < 7; ++i) {
+    s.k0[i] = uint32_t(seed) + i * 0x9E3779B9u;
+    s.k1[i] = uint32_t(seed >> 32) + i * 0xBB67AE85u;
   }
-  return make_uint4(c0, c1, c2, c3);
+  const uint64_t b = (off & 0xFFFFFFFFu) * 0xCD9E8D57u;
+  s.o_hi = uint32_t(b >> 32);
+  s.o_lo = uint32_t(b);
+  s.o1 = uint32_t(off >> 32);
+  s.thr_hi = d.thr << 16;
+  return s;
 }
 
 // The random block of the 8 elements (row, 8 c8 .. 8 c8 + 7).
 __device__ __forceinline__ uint4 drop_block(const DropState& s, uint32_t c8, uint32_t row) {
-  return philox4x32_7(c8, row, s.o0, s.o1, s.k0, s.k1);
+  const uint64_t a0 = uint64_t(c8) * 0xD2511F53u;
+  uint32_t c0 = s.o_hi ^ row ^ s.k0[0], c1 = s.o_lo;
+  uint32_t c2 = uint32_t(a0 >> 32) ^ s.o1 ^ s.k1[0], c3 = uint32_t(a0);
+#pragma unroll
+  for (int i = 1; i < 7; ++i) {
+    const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
+    c0 = uint32_t(b >> 32) ^ c1 ^ s.k0[i];
+    c2 = uint32_t(a >> 32) ^ c3 ^ s.k1[i];
+    c1 = uint32_t(b);
+    c3 = uint32_t(a);
+  }
+  return make_uint4(c0, c1, c2, c3);
 }
 
 // Zero the dropped ones of two bf16 values packed in `x` (`w` holds their

@@ -430,6 +430,22 @@ __device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, 
       : "memory");
 }
 
+// The single-CTA forms of the two.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::
+          "r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
 // Instruction descriptor for kind::mxf8f6f4 with e4m3 A/B, e8m0 scales and
 // fp32 D:
 //   [4,6) scale byte of B's 32-bit words, [7,10) A fmt (0 = e4m3), [10,13) B
@@ -438,6 +454,13 @@ __device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, 
 __host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t M, uint32_t N, bool a_mn, bool b_mn, uint32_t sf_id) {
   return (sf_id << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | ((N >> 3) << 17) | (1u << 23) |
          ((M >> 4) << 24) | (sf_id << 29);
+}
+
+// 4-byte load from another CTA's shared memory (shared::cluster address).
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
 }
 
 // 16-byte shared-memory load and store by 32-bit address.
