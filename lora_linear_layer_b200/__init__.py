@@ -467,7 +467,8 @@ def lora_restore(W_src, W_dst, stream=None) -> None:
 
 # ------------------------------------- dropout and the 8-bit base ----
 
-def _check_typed(t, name: str, dtype, shape: Tuple[int, ...], device):
+def _bad(t, name: str, dtype, shape: Tuple[int, ...], device):
+    """Raises what is wrong with an argument that _ok refused."""
     torch = _tm()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -479,43 +480,51 @@ def _check_typed(t, name: str, dtype, shape: Tuple[int, ...], device):
         raise ValueError(f"{name} must be contiguous")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _workspace_arg(workspace, device):
+def _arg(t, name: str, dtype, shape: Tuple[int, ...], index: int):
+    """The pointer of a contiguous tensor of this type and shape on CUDA
+    device ``index``.  (One expression for the usual case: a call checks ten
+    tensors, which is host time of the order of a small layer's kernels.)"""
+    try:
+        if t.dtype is dtype and t.get_device() == index and index >= 0 and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _bad(t, name, dtype, shape, f"cuda:{index}")
+
+
+def _workspace_arg(workspace, index: int):
     torch = _tm()
     if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
-    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
-
-
-def _rng_arg(rng, device):
-    if rng is None:
-        return None
-    _check_typed(rng, "rng", _tm().int64, (2,), device)
-    return _ptr(rng)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{index}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _scales_shape(d_out: int, d_in: int) -> Tuple[int, int]:
     return (d_out + 127) // 128, (d_in + 127) // 128
 
 
-def _on_device(device, stream, call):
-    """call(stream handle) with `device` current (the library launches on the
-    current device)."""
+def _call(name, index: int, args, stream):
+    """Calls the library's function `name` with `args` and the stream, with
+    the tensors' device current (the library launches on the current one)."""
     torch = _tm()
-    if device.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+    fn = getattr(lib(), name)
+    if index == torch._C._cuda_getDevice():
+        code = fn(*args, _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream))
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, _stream(stream))
+    if code != 0:
+        raise LoraError(code, name)
 
 
-def _layer_args(X, W, Ws, A, B, rng, workspace, outs, grads=()):
-    """Checks the tensors of a layer call, all on X's device; returns their
-    pointers, the sizes and the rng and workspace arguments."""
+def _layer(name, X, W, Ws, A, B, outs, scale, p, rng, workspace, flags, stream):
+    """A layer call: checks the tensors, all on X's device; `outs` are the
+    tensors after B, as (name, tensor, dtype)."""
     torch = _tm()
     bf16 = torch.bfloat16
     if not isinstance(X, torch.Tensor) or not isinstance(B, torch.Tensor):
@@ -524,53 +533,45 @@ def _layer_args(X, W, Ws, A, B, rng, workspace, outs, grads=()):
         raise ValueError(f"X and B must be 2-D, got {X.dim()}-D and {B.dim()}-D")
     M, d_in = X.shape
     d_out, r = B.shape
-    dev = X.device
-    shapes = {"X": (M, d_in), "A": (r, d_in), "B": (d_out, r), "Y": (M, d_out), "dY": (M, d_out), "dX": (M, d_in),
-              "dA": (r, d_in), "dB": (d_out, r)}
-    _check_typed(X, "X", bf16, shapes["X"], dev)
-    ptrs = [_ptr(X)]
+    i = X.get_device()
+    args = [_arg(X, "X", bf16, (M, d_in), i)]
     if Ws is None:
-        _check_typed(W, "W", bf16, (d_out, d_in), dev)
-        ptrs.append(_ptr(W))
+        args.append(_arg(W, "W", bf16, (d_out, d_in), i))
     else:
-        _check_typed(W, "Wq", torch.float8_e4m3fn, (d_out, d_in), dev)
-        _check_typed(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), dev)
-        ptrs += [_ptr(W), _ptr(Ws)]
-    for name, t, dtype in (("A", A, bf16), ("B", B, bf16)) + tuple(outs) + tuple(grads):
-        _check_typed(t, name, dtype, shapes[name], dev)
-        ptrs.append(_ptr(t))
-    return ptrs, (M, d_in, d_out, r), _rng_arg(rng, dev), _workspace_arg(workspace, dev)
+        args.append(_arg(W, "Wq", torch.float8_e4m3fn, (d_out, d_in), i))
+        args.append(_arg(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), i))
+    args.append(_arg(A, "A", bf16, (r, d_in), i))
+    args.append(_arg(B, "B", bf16, (d_out, r), i))
+    for n, t, dtype in outs:
+        shape = (r, d_in) if n == "dA" else (d_out, r) if n == "dB" else (M, d_in) if n == "dX" else (M, d_out)
+        args.append(_arg(t, n, dtype, shape, i))
+    args += (M, d_in, d_out, r, scale, p, None if rng is None else _arg(rng, "rng", torch.int64, (2,), i))
+    args += _workspace_arg(workspace, i)
+    if flags is not None:
+        args.append(flags)
+    _call(name, i, args, stream)
 
 
-def _adapter_fwd(name, X, W, Ws, A, B, Y, scale, p, rng, workspace, stream):
-    ptrs, sizes, rng_ptr, ws = _layer_args(X, W, Ws, A, B, rng, workspace, (("Y", Y, _tm().bfloat16),))
-    fn = getattr(lib(), name)
-    _raise(_on_device(X.device, stream, lambda st: fn(*ptrs, *sizes, float(scale), float(p), rng_ptr, *ws, st)), name)
-
-
-def _adapter_bwd(name, X, W, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream):
+def _layer_bwd(name, X, W, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream):
     torch = _tm()
-    gdt = torch.float32 if int(flags) & LORA_BWD_FP32_GRADS else torch.bfloat16
-    ptrs, sizes, rng_ptr, ws = _layer_args(
-        X, W, Ws, A, B, rng, workspace, (("dY", dY, torch.bfloat16), ("dX", dX, torch.bfloat16)),
-        (("dA", dA, gdt), ("dB", dB, gdt)))
-    fn = getattr(lib(), name)
-    _raise(_on_device(X.device, stream,
-                      lambda st: fn(*ptrs, *sizes, float(scale), float(p), rng_ptr, *ws, int(flags), st)), name)
+    bf16 = torch.bfloat16
+    gdt = torch.float32 if int(flags) & LORA_BWD_FP32_GRADS else bf16
+    _layer(name, X, W, Ws, A, B, (("dY", dY, bf16), ("dX", dX, bf16), ("dA", dA, gdt), ("dB", dB, gdt)), scale, p, rng,
+           workspace, int(flags), stream)
 
 
 def lora_fwd_dropout(X, W, A, B, Y, scale: float, p: float, rng, workspace, stream=None) -> None:
     """Y = X W^T + T B^T with T = scale/(1-p) (m * X) A^T, the mask m drawn
     from ``rng``, an int64 CUDA tensor [seed, offset] (see include/lora.h).
     ``workspace`` (lora_bwd_workspace_size bytes) receives T."""
-    _adapter_fwd("lora_fwd_dropout", X, W, None, A, B, Y, scale, p, rng, workspace, stream)
+    _layer("lora_fwd_dropout", X, W, None, A, B, (("Y", Y, _tm().bfloat16),), scale, p, rng, workspace, None, stream)
 
 
 def lora_bwd_dropout(X, W, A, B, dY, dX, dA, dB, scale: float, p: float, rng, workspace, flags: int = 0,
                      stream=None) -> None:
     """The backward of lora_fwd_dropout for the same ``rng`` values; with
     LORA_BWD_T_SAVED the workspace is the one the forward left T in."""
-    _adapter_bwd("lora_bwd_dropout", X, W, None, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
+    _layer_bwd("lora_bwd_dropout", X, W, None, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
 
 
 def lora_fp8_workspace_size(M: int, d_in: int, d_out: int, r: int) -> int:
@@ -581,41 +582,35 @@ def lora_fwd_fp8(X, Wq, Ws, A, B, Y, scale: float, workspace, p: float = 0.0, rn
     """Y = Xq Wq^T + T B^T over an 8-bit base: Wq float8_e4m3fn [d_out, d_in],
     Ws float8_e8m0fnu [ceil(d_out/128), ceil(d_in/128)] (see include/lora.h);
     ``workspace`` of lora_fp8_workspace_size bytes."""
-    _adapter_fwd("lora_fwd_fp8", X, Wq, Ws, A, B, Y, scale, p, rng, workspace, stream)
+    _layer("lora_fwd_fp8", X, Wq, Ws, A, B, (("Y", Y, _tm().bfloat16),), scale, p, rng, workspace, None, stream)
 
 
 def lora_bwd_fp8(X, Wq, Ws, A, B, dY, dX, dA, dB, scale: float, workspace, p: float = 0.0, rng=None, flags: int = 0,
                  stream=None) -> None:
     """The backward of lora_fwd_fp8: dX through Wq, dA and dB of the adapter."""
-    _adapter_bwd("lora_bwd_fp8", X, Wq, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
+    _layer_bwd("lora_bwd_fp8", X, Wq, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
 
 
-def _quant_args(W, Wq, Ws):
+def _quant(name, W, Wq, Ws, order, stream):
     torch = _tm()
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be a 2-D tensor")
     d_out, d_in = W.shape
-    _check_typed(W, "W", torch.bfloat16, (d_out, d_in), W.device)
-    _check_typed(Wq, "Wq", torch.float8_e4m3fn, (d_out, d_in), W.device)
-    _check_typed(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), W.device)
-    return d_out, d_in
+    i = W.get_device()
+    p = (_arg(W, "W", torch.bfloat16, (d_out, d_in), i), _arg(Wq, "Wq", torch.float8_e4m3fn, (d_out, d_in), i),
+         _arg(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), i))
+    _call(name, i, (p[order[0]], p[order[1]], p[order[2]], d_out, d_in), stream)
 
 
 def lora_quantize_fp8(W, Wq, Ws, stream=None) -> None:
     """W (bf16) -> Wq (e4m3 codes) and Ws (one power of two for each
     128 x 128 block; see include/lora.h)."""
-    d_out, d_in = _quant_args(W, Wq, Ws)
-    fn = lib().lora_quantize_fp8
-    _raise(_on_device(W.device, stream, lambda st: fn(_ptr(W), _ptr(Wq), _ptr(Ws), d_out, d_in, st)),
-           "lora_quantize_fp8")
+    _quant("lora_quantize_fp8", W, Wq, Ws, (0, 1, 2), stream)
 
 
 def lora_dequantize_fp8(Wq, Ws, W, stream=None) -> None:
     """Wq, Ws -> the bf16 values they stand for."""
-    d_out, d_in = _quant_args(W, Wq, Ws)
-    fn = lib().lora_dequantize_fp8
-    _raise(_on_device(W.device, stream, lambda st: fn(_ptr(Wq), _ptr(Ws), _ptr(W), d_out, d_in, st)),
-           "lora_dequantize_fp8")
+    _quant("lora_dequantize_fp8", W, Wq, Ws, (1, 2, 0), stream)
 
 
 def lora_get_device_status() -> int:

@@ -80,11 +80,14 @@ void pick_pass(int64_t rows, int64_t K, int r, bool p_mn, bool r_mn, int out_mod
   a.n_rchunks = (r_pad + c.RCW - 1) / c.RCW;
   a.stages = 3;
   c.smem = PassLayout(p_mn, r_mn, c.RCW, r_pad, a.n_rchunks, a.stages).total + 1024;
-  const int per_sm = std::max(1, std::min<int>(int(kSmemPerSM / (c.smem + 1024)), 2048 / kPassThreads));
+  const int per_sm = std::max(1, std::min<int>(int(kSmemPerSM / (c.smem + 1024)), 2048 / pass_threads(c.RCW, p_mn)));
   const int block_k = p_mn ? 64 : 128;
   const int nb = int((K + block_k - 1) / block_k);
   const int tiles = int(std::max<int64_t>(1, launch_tiles));
-  int splits = std::max(1, std::min({per_sm * sm_count / tiles, 8, std::max(1, nb * block_k / 256)}));
+  // (one block an SM: clusters of 8 leave SMs of a GPC idle, so that 17 row
+  // tiles took two rounds, 28 us on X[2051, 2560] at r = 128)
+  const int most = per_sm == 1 ? 4 : 8;
+  int splits = std::max(1, std::min({per_sm * sm_count / tiles, most, std::max(1, nb * block_k / 256)}));
   a.nb_per_split = std::max(1, (nb + splits - 1) / splits);
   splits = std::max(1, (nb + a.nb_per_split - 1) / a.nb_per_split);
   a.rows = int32_t(rows);
@@ -124,7 +127,7 @@ lora_status_t launch_pass_t(const PassMaps& m0, const PassCfg& c0, const PassMap
   const dim3 cl(1, unsigned(c0.args.splits), 1);
   const PassMaps& second = m1 != nullptr ? *m1 : m0;
   const int ta = atoms.bytes != nullptr ? kAtomBlocks : 0;
-  return launch_ex("adapter pass", kern, dim3(unsigned(t0 + t1 + ta), unsigned(c0.args.splits)), dim3(kPassThreads),
+  return launch_ex("adapter pass", kern, dim3(unsigned(t0 + t1 + ta), unsigned(c0.args.splits)), dim3(pass_threads(RCW, P_MN)),
                    smem, st, &cl, m0.p, m0.r, second.p, second.r, c0.args, c1 != nullptr ? c1->args : c0.args,
                    int32_t(t0), int32_t(t0 + t1), atoms);
 }
@@ -180,14 +183,18 @@ uint32_t lr_stage_bytes(bool fp8, bool mn, int BN) {
 }
 
 // OUT[M, N] over the contraction K: the wide tile (224 columns for 8 bits,
-// 256 for bf16) unless 128-wide ones finish sooner, at a cost of FIX columns
-// more each.
+// 256 for bf16) or 128 columns, whichever needs fewer rounds of the clusters.
+// A round takes nearly the same time with either (what bounds one tile a pair
+// is its operands' way from L2; X[2048, 4096], N = 4096: 4 rounds of 128 in 49
+// us, 3 of 224 in 38 us at 8 bits, 4 in 81 and 2 of 256 in 50 us for bf16); at
+// equal rounds the narrow one is a little shorter (512 x 4096 x 4096 bf16: 25
+// against 28 us).
 void pick_lr(int64_t M, int64_t N, int64_t K, int r, bool fp8, bool mn, int sm_count, LrCfg& c) {
   const int64_t clusters = sm_count / 2;
   const int64_t num_m = (M + 255) / 256;
   auto cost = [&](int bn) {
     const int64_t tiles = num_m * ((N + bn - 1) / bn);
-    return ((tiles + clusters - 1) / clusters) * int64_t(bn + 64);
+    return ((tiles + clusters - 1) / clusters) * int64_t(bn + 1024);
   };
   const int wide = fp8 ? 224 : 256;
   c.BN = cost(128) < cost(wide) ? 128 : wide;
@@ -222,7 +229,7 @@ lora_status_t launch_lr_t(const CUtensorMap* maps, const LrCfg& c, int sm_count,
   const int64_t tiles = int64_t(c.args.f.num_m) * c.args.f.num_n;
   const int clusters = int(std::min<int64_t>(tiles, max_clusters(kern, 2, c.smem, sm_count)));
   const dim3 cl(2, 1, 1);
-  return launch_ex("low-rank GEMM", kern, dim3(unsigned(clusters * 2)), dim3(kFusedThreads), c.smem, st, &cl,
+  return launch_ex("low-rank GEMM", kern, dim3(unsigned(clusters * 2)), dim3(lr_threads(DROP)), c.smem, st, &cl,
                    maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], c.args);
 }
 
@@ -417,7 +424,7 @@ lora_status_t adapter_fwd_run(const void* X, const Base& W, const void* A, const
 
 // Backward.  Arguments already validated.
 //  1. T unless saved, and dT = s dY B (with an 8-bit base also dY's codes);
-//  2. dB = dY^T T and dA = dT^T (m * X)/(1-p), one launch;
+//  2. dB = dY^T T and dA = dT^T (m * X)/(1-p);
 //  3. dX.
 lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const void* B, const void* dY, void* dX,
                               void* dA, void* dB, int64_t M, int64_t d_in, int64_t d_out, int32_t r, float scale,
@@ -465,11 +472,14 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
     if (s != LORA_OK) return s;
   }
   {
+    // One launch, dA's row tiles first: with a mask a stage of theirs takes
+    // twice dB's time (16384 x 4096 x 14336, r = 64, p = 0.1: 142 us against
+    // 215 us with dB's first, and 187 us as two launches).
     PassCfg cb, ca;
     const int64_t tiles = (d_out + 127) / 128 + (d_in + 127) / 128;
-    pick_pass(d_out, M, r, true, true, OUT_ROWS_R, tiles, sms, cb);
     pick_pass(d_in, M, r, true, true, OUT_COLS_R, tiles, sms, ca);
-    resplit_pass(ca, cb.args.splits, true);
+    pick_pass(d_out, M, r, true, true, OUT_ROWS_R, tiles, sms, cb);
+    resplit_pass(cb, ca.args.splits, true);
     cb.args.out = reinterpret_cast<__nv_bfloat16*>(dB);
     cb.args.out_f32 = f32 ? 1 : 0;
     ca.args.out = reinterpret_cast<__nv_bfloat16*>(dA);
@@ -482,7 +492,7 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
         !make_map(&ma.p, X, d_in, M, d_in, 64, 64, 128) ||
         !make_map(&ma.r, at.dT, r_pad, M, r_pad, rcw, 64, rcw * 2))
       return LORA_ERR_CUDA;
-    if ((s = launch_pass<true, false>(mb, cb, st, &ma, &ca)) != LORA_OK) return s;
+    if ((s = launch_pass<true, false>(ma, ca, st, &mb, &cb)) != LORA_OK) return s;
   }
   return launch_dx(dY, at.q, W, A, dX, at.dT, c, r, sms, st);
 }

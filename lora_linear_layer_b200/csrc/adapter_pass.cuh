@@ -29,8 +29,11 @@
 
 namespace lora {
 
-constexpr int kPassWorkers = 8;                       // warps that work on the stages
-constexpr int kPassThreads = 64 + 32 * kPassWorkers;  // + TMA warp + MMA warp
+// Warps that work on the stages, beside the TMA and the MMA warp: 8, and two
+// blocks an SM, while the rank's operand is narrow; above r = 32 K-major
+// stages are 48 KB and more, one block fits an SM, and it gets 16.
+__host__ __device__ constexpr int pass_workers(int rcw, bool p_mn) { return rcw == 64 && !p_mn ? 16 : 8; }
+__host__ __device__ constexpr int pass_threads(int rcw, bool p_mn) { return 64 + 32 * pass_workers(rcw, p_mn); }
 
 struct PassArgs {
   int32_t rows;           // output rows (size of the i dimension)
@@ -68,12 +71,13 @@ struct PassLayout {
 };
 
 template <bool P_MN, int RCW, bool QUANT>
-__global__ void __launch_bounds__(kPassThreads, 2)
+__global__ void __launch_bounds__(pass_threads(RCW, P_MN), pass_workers(RCW, P_MN) == 16 ? 1 : 2)
     adapter_pass_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmR0,
                         const __grid_constant__ CUtensorMap tmP1, const __grid_constant__ CUtensorMap tmR1,
                         const __grid_constant__ PassArgs a0, const __grid_constant__ PassArgs a1,
                         const int32_t x_split, const int32_t x_atoms, const __grid_constant__ ScaleAtomArgs atoms) {
   static_assert(!(P_MN && QUANT), "codes are written row by row");
+  constexpr int kPassWorkers = pass_workers(RCW, P_MN), kPassThreads = pass_threads(RCW, P_MN);
   if constexpr (QUANT) {
     if (int(blockIdx.x) >= x_atoms) {  // blocks behind the row tiles: the other operand's scales
       griddep_wait();
@@ -121,6 +125,10 @@ __global__ void __launch_bounds__(kPassThreads, 2)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(second ? &tmP1 : &tmP0);
+    tma_prefetch_desc(second ? &tmR1 : &tmR0);
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), ncols);

@@ -6,8 +6,8 @@
 //   dX = dYq Wq   + m * (dT A)/(1-p)
 // One accumulator holds both products.  The rank side is one or two K blocks
 // of the same ring, issued before the base blocks: where the mask m applies
-// to it alone (DROP), the epilogue warps take the rank product out of TMEM,
-// mask and scale it, and put it back, and the base product then accumulates
+// to it alone (DROP), eight warps take the rank product out of TMEM, mask and
+// scale it, and put it back, and the base product then accumulates
 // onto it.  That costs no extra accumulator and no extra pass over OUT, and
 // it hides behind another tile's K loop: the rank blocks of the next tile
 // are issued in the middle of the current one, into the other accumulator.
@@ -91,8 +91,13 @@ struct LrLayout {
   }
 };
 
+// Warps 0 TMA, 1 MMA, 2-5 epilogue, and with DROP 6-13 the mask: with the
+// epilogue's warps for it a tile of 1024 contracted values took 7.5 us, mask
+// and store one after the other, where its products take 5.
+constexpr int lr_threads(bool drop) { return kFusedThreads + (drop ? 256 : 0); }
+
 template <bool FP8, bool MN, bool DROP, int BN>
-__global__ void __launch_bounds__(kFusedThreads, 1)
+__global__ void __launch_bounds__(lr_threads(DROP), 1)
     lowrank_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmPS,
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       mbar_init(accempty0 + 8u * b, 8);
     }
     mbar_init(rankfull, 1);
-    mbar_init(masked, 8);
+    mbar_init(masked, 16);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -344,60 +349,17 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       G::commit_local(drain);
       wait_bounded(drain, 0u, abort_flag, lim, SITE_DRAIN, false);
     }
-  } else {
+  } else if (warp < 6) {
     // ---------------------------------------------------- epilogue ----
     const int q = warp & 3;            // TMEM lane quarter of this warp
     const uint32_t lane_base = uint32_t(q * 32) << 16;
     LrSched sch(la, n_clusters, cluster_id);
-    uint32_t ranks = 0, full_waits[2] = {0u, 0u};
+    uint32_t full_waits[2] = {0u, 0u};
     const uint32_t ep_off = L.off_ep + uint32_t(q * a.ep_bufs) * kEpBufBytes;
     uint32_t epc = 0;  // output blocks staged so far
-    DropState ds{};
-    if constexpr (DROP) ds = drop_load(la.drop);
-    // DROP: mask and scale the rank product in accumulator b, tile (m, n)
-    auto mask_tile = [&](uint32_t b, int m, int n) -> bool {
-      if (!warp_wait_bounded(rankfull, ranks++ & 1u, abort_flag, lim, SITE_TFULL, true)) return false;
-      tc_fence_after();
-      const uint32_t row = uint32_t(m * 256 + int(rank) * kBM + q * 32 + lane);
-#pragma unroll 1
-      for (int ch = 0; ch < BN / 32; ++ch) {
-        const uint32_t col = tmem + lane_base + b * BN + uint32_t(ch * 32);
-        uint32_t v[32];
-        tmem_ld_x32(col, v);
-        const uint32_t c8 = uint32_t(n * BN + ch * 32) / 8u;
-        uint4 r[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) r[g] = drop_block(ds, c8 + g, row);
-        tmem_ld_wait();
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t w[4] = {r[g].x, r[g].y, r[g].z, r[g].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float lo = __uint_as_float(v[8 * g + 2 * i]) * la.drop.inv_keep;
-            const float hi = __uint_as_float(v[8 * g + 2 * i + 1]) * la.drop.inv_keep;
-            v[8 * g + 2 * i] = (w[i] << 16) < ds.thr_hi ? 0u : __float_as_uint(lo);
-            v[8 * g + 2 * i + 1] = w[i] < ds.thr_hi ? 0u : __float_as_uint(hi);
-          }
-        }
-        tmem_st_x32(col, v);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) G::arrive_leader(masked);
-      return true;
-    };
-    int m, n, mn = 0, nn = 0;
-    bool have = sch.next(m, n);
+    int m, n;
     uint32_t b = 0;
-    bool ok = true;
-    if constexpr (DROP) ok = !have || mask_tile(0, m, n);
-    while (ok && have) {
-      const bool more = sch.next(mn, nn);
-      if constexpr (DROP) {
-        if (more && !mask_tile(b ^ 1u, mn, nn)) break;
-      }
+    while (sch.next(m, n)) {
       const uint32_t fpar = (b ? full_waits[1]++ : full_waits[0]++) & 1u;
       if (!warp_wait_bounded(accfull0 + 8u * b, fpar, abort_flag, lim, SITE_ACCFULL, true)) break;
       tc_fence_after();
@@ -439,11 +401,51 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       __syncwarp();
       if (lane == 0) G::arrive_leader(accempty0 + 8u * b);
       b ^= 1u;
-      m = mn;
-      n = nn;
-      have = more;
     }
     if (lane == 0) bulk_wait_group0();  // every output store has completed
+  } else if constexpr (DROP) {
+    // -------------------------------------------------------- mask ----
+    // Two warps a lane quarter, every other 32 columns each.
+    const int q = warp & 3;
+    const uint32_t lane_base = uint32_t(q * 32) << 16;
+    LrSched sch(la, n_clusters, cluster_id);
+    const DropState ds = drop_load(la.drop);
+    int m, n;
+    uint32_t tiles = 0;
+    while (sch.next(m, n)) {
+      const uint32_t b = tiles & 1u;
+      if (!warp_wait_bounded(rankfull, tiles & 1u, abort_flag, lim, SITE_TFULL, true)) break;
+      ++tiles;
+      tc_fence_after();
+      const uint32_t row = uint32_t(m * 256 + int(rank) * kBM + q * 32 + lane);
+#pragma unroll 1
+      for (int ch = (warp - 6) >> 2; ch < BN / 32; ch += 2) {
+        const uint32_t col = tmem + lane_base + b * BN + uint32_t(ch * 32);
+        uint32_t v[32];
+        tmem_ld_x32(col, v);
+        const uint32_t c8 = uint32_t(n * BN + ch * 32) / 8u;
+        uint4 r[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) r[g] = drop_block(ds, c8 + g, row);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t w[4] = {r[g].x, r[g].y, r[g].z, r[g].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = __uint_as_float(v[8 * g + 2 * i]) * la.drop.inv_keep;
+            const float hi = __uint_as_float(v[8 * g + 2 * i + 1]) * la.drop.inv_keep;
+            v[8 * g + 2 * i] = (w[i] << 16) < ds.thr_hi ? 0u : __float_as_uint(lo);
+            v[8 * g + 2 * i + 1] = w[i] < ds.thr_hi ? 0u : __float_as_uint(hi);
+          }
+        }
+        tmem_st_x32(col, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) G::arrive_leader(masked);
+    }
   }
 
   tc_fence_before();

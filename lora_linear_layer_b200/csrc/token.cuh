@@ -221,6 +221,12 @@ __global__ void __launch_bounds__(kStreamThreads)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmT);
+  }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), ncols);
     tmem_relinquish();
