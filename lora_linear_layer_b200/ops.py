@@ -25,6 +25,15 @@ torch._dynamo.explain).  Here:
   ``lora_linear_train`` are differentiable in X, A and B through their
   backward ops.  W is frozen: it gets no gradient.
 
+* ``torch.ops.lora_b200.lora_linear_adapter(X, W, W_scales, A, B, scale, p,
+  rng)`` is the layer with dropout on the adapter branch (``lora_fwd_dropout``)
+  or, with ``W_scales`` (W then holds e4m3 codes), over an 8-bit base
+  (``lora_fwd_fp8``), with or without dropout.  It returns (Y, saved), saved
+  being T for ``lora_linear_adapter_bwd``.  The mask is drawn from ``rng``, an
+  int64 tensor [seed, offset] on the device, and never stored: the backward
+  draws it again.  ``quantize_weight`` and ``dequantize_weight`` convert a
+  weight.
+
 The scale is passed explicitly, so rsLoRA's alpha / sqrt(r) (unsloth fork
 commit log, scripts/benchmarks/qwen3_flex_inference.py: PEFT keeps the
 adapter's scaling, alpha / sqrt(r) under rsLoRA, in the module) is as easy
@@ -41,8 +50,9 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import (LORA_BWD_FP32_GRADS, LORA_BWD_T_SAVED, lora_bwd_scaled, lora_bwd_workspace_size, lora_fwd_save_scaled,
-               lora_fwd_scaled)
+from . import (LORA_BWD_FP32_GRADS, LORA_BWD_T_SAVED, lora_bwd_dropout, lora_bwd_fp8, lora_bwd_scaled,
+               lora_bwd_workspace_size, lora_dequantize_fp8, lora_fp8_workspace_size, lora_fwd_dropout, lora_fwd_fp8,
+               lora_fwd_save_scaled, lora_fwd_scaled, lora_quantize_fp8)
 
 _LIB = "lora_b200"
 
@@ -187,17 +197,143 @@ def _backward(ctx, dY):
 lora_linear.register_autograd(_backward, setup_context=_setup_context)
 
 
+# ------------------------------------- dropout and the 8-bit base ----
+
+def quantize_weight(W: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(codes float8_e4m3fn [d_out, d_in], scales float8_e8m0fnu, one power of
+    two for each 128 x 128 block) of a bf16 weight (``lora_quantize_fp8``)."""
+    d_out, d_in = W.shape
+    codes = torch.empty((d_out, d_in), dtype=torch.float8_e4m3fn, device=W.device)
+    scales = torch.empty(((d_out + 127) // 128, (d_in + 127) // 128), dtype=torch.float8_e8m0fnu, device=W.device)
+    lora_quantize_fp8(W.contiguous(), codes, scales)
+    return codes, scales
+
+
+def dequantize_weight(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """The bf16 weight that codes and scales stand for (``lora_dequantize_fp8``)."""
+    W = torch.empty(codes.shape, dtype=torch.bfloat16, device=codes.device)
+    lora_dequantize_fp8(codes, scales, W)
+    return W
+
+
+def _saved_bytes(M, r: int, fp8: bool):
+    """Bytes that the forward leaves for the backward: lora_bwd's workspace,
+    or with an 8-bit base the T at its start alone (the rest of that workspace
+    is scratch of M * max(d_in, d_out) bytes, not worth keeping)."""
+    return _workspace_bytes(M, r) // 2 if fp8 else _workspace_bytes(M, r)
+
+
+def _check_rng(p: float, rng: Optional[torch.Tensor]):
+    if p > 0 and rng is None:
+        raise ValueError("dropout needs rng, an int64 tensor [seed, offset] on the layer's device")
+
+
+@torch.library.custom_op(f"{_LIB}::lora_linear_adapter", mutates_args=())
+def lora_linear_adapter(X: torch.Tensor, W: torch.Tensor, W_scales: Optional[torch.Tensor], A: torch.Tensor,
+                        B: torch.Tensor, scale: float, p: float,
+                        rng: Optional[torch.Tensor]) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(Y, saved): Y = X W^T + T B^T, T = scale/(1-p) (m * X) A^T, over a bf16
+    base or, with W_scales, over e4m3 codes W."""
+    M, d_in, d_out, r = _check(X, W, A, B)
+    _check_rng(p, rng)
+    fp8 = W_scales is not None
+    nbytes = lora_fp8_workspace_size(M, d_in, d_out, r) if fp8 else _workspace_bytes(M, r)
+    if not fp8 and nbytes < lora_bwd_workspace_size(M, d_in, d_out, r):
+        raise RuntimeError("lora_linear_adapter: the library needs a larger workspace than its documented layout")
+    Y = torch.empty((M, d_out), dtype=X.dtype, device=X.device)
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=X.device)
+    args = (X.contiguous(), W.contiguous())
+    ab = (A.contiguous(), B.contiguous(), Y, scale)
+    if fp8:
+        lora_fwd_fp8(*args, W_scales.contiguous(), *ab, ws, p, rng)
+        return Y, ws[:max(_saved_bytes(M, r, True), 1)].clone()
+    lora_fwd_dropout(*args, *ab, p, rng, ws)
+    return Y, ws
+
+
+@lora_linear_adapter.register_fake
+def _lora_linear_adapter_fake(X, W, W_scales, A, B, scale, p, rng):
+    M, d_in, d_out, r = _check(X, W, A, B)
+    _check_rng(p, rng)
+    nbytes = _saved_bytes(M, r, W_scales is not None)
+    return X.new_empty((M, d_out)), X.new_empty((max(nbytes, 1),), dtype=torch.uint8)
+
+
+@torch.library.custom_op(f"{_LIB}::lora_linear_adapter_bwd", mutates_args=("saved",))
+def lora_linear_adapter_bwd(X: torch.Tensor, W: torch.Tensor, W_scales: Optional[torch.Tensor], A: torch.Tensor,
+                            B: torch.Tensor, dY: torch.Tensor, saved: torch.Tensor, scale: float, p: float,
+                            rng: Optional[torch.Tensor],
+                            fp32_grads: bool = False) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dX, dA, dB) of lora_linear_adapter for the same rng values; T is taken
+    from ``saved`` (over a bf16 base dT is written beside it)."""
+    M, d_in, d_out, r = _check(X, W, A, B)
+    gdt = torch.float32 if fp32_grads else A.dtype
+    dX = torch.empty((M, d_in), dtype=X.dtype, device=X.device)
+    dA = torch.empty((r, d_in), dtype=gdt, device=A.device)
+    dB = torch.empty((d_out, r), dtype=gdt, device=B.device)
+    flags = LORA_BWD_T_SAVED | (LORA_BWD_FP32_GRADS if fp32_grads else 0)
+    args = (X.contiguous(), W.contiguous())
+    rest = (A.contiguous(), B.contiguous(), dY.contiguous(), dX, dA, dB, scale)
+    if W_scales is not None:
+        ws = torch.empty(max(lora_fp8_workspace_size(M, d_in, d_out, r), 1), dtype=torch.uint8, device=X.device)
+        ws[:saved.numel()].copy_(saved)
+        lora_bwd_fp8(*args, W_scales.contiguous(), *rest, ws, p, rng, flags)
+    else:
+        lora_bwd_dropout(*args, *rest, p, rng, saved, flags)
+    return dX, dA, dB
+
+
+@lora_linear_adapter_bwd.register_fake
+def _lora_linear_adapter_bwd_fake(X, W, W_scales, A, B, dY, saved, scale, p, rng, fp32_grads=False):
+    return _lora_linear_bwd_fake(X, W, A, B, dY, scale, fp32_grads)
+
+
+def _setup_context_adapter(ctx, inputs, output):
+    X, W, W_scales, A, B, scale, p, rng = inputs
+    if W.requires_grad:
+        raise RuntimeError("lora_linear: the base weight W is frozen and gets no gradient; "
+                           "call W.requires_grad_(False)")
+    ctx.save_for_backward(X, W, W_scales, A, B, rng, output[1])
+    ctx.scale, ctx.p = scale, p
+
+
+def _backward_adapter(ctx, dY, _d_saved):
+    X, W, W_scales, A, B, rng, saved = ctx.saved_tensors
+    dX, dA, dB = torch.ops.lora_b200.lora_linear_adapter_bwd(X, W, W_scales, A, B, dY.contiguous(), saved, ctx.scale,
+                                                             ctx.p, rng)
+    need = ctx.needs_input_grad
+    return (dX if need[0] else None, None, None, dA if need[3] else None, dB if need[4] else None, None, None, None)
+
+
+lora_linear_adapter.register_autograd(_backward_adapter, setup_context=_setup_context_adapter)
+
+
 class LoRALinear(torch.nn.Module):
     """A linear layer with a frozen base weight and a trainable rank-r adapter:
     y = x W^T + s (x A^T) B^T over the last dimension of x (any leading
     dimensions).  s = alpha / r, or alpha / sqrt(r) with ``rslora=True``.
     A is initialised N(0, 1/d_in) (variance), B to zero (the adapter starts
-    as the identity map of the base layer); all parameters are bf16."""
+    as the identity map of the base layer); all parameters are bf16.
+
+    ``dropout``: in training the adapter (not the base) sees x with each value
+    dropped with this probability and the rest scaled by 1/(1 - dropout).  The
+    mask's seed and offset are drawn from torch's generator of the device for
+    each call, so torch.manual_seed repeats a run, activation checkpointing
+    repeats a mask, and a captured step draws a new mask at each replay.
+
+    ``quantize_base()`` turns the base weight into 8 bits (e4m3 codes, one
+    power-of-two scale for each 128 x 128 block), as buffers ``weight_codes``
+    and ``weight_scales`` in place of ``weight``: half the memory, and 8-bit
+    products in forward and backward."""
 
     def __init__(self, d_in: int, d_out: int, r: int, alpha: float, rslora: bool = False,
-                 device: Optional[torch.device] = None, generator: Optional[torch.Generator] = None):
+                 device: Optional[torch.device] = None, generator: Optional[torch.Generator] = None,
+                 dropout: float = 0.0):
         super().__init__()
         self.d_in, self.d_out, self.r, self.alpha = int(d_in), int(d_out), int(r), float(alpha)
+        if not 0.0 <= dropout < 1.0:
+            raise ValueError(f"dropout must be in [0, 1), got {dropout}")
+        self.dropout = float(dropout)
         self.scale = self.alpha / (math.sqrt(self.r) if rslora else self.r)
         kw = dict(dtype=torch.bfloat16, device=device)
         self.weight = torch.nn.Parameter(
@@ -205,10 +341,30 @@ class LoRALinear(torch.nn.Module):
         self.lora_A = torch.nn.Parameter((torch.randn(r, d_in, generator=generator) * d_in ** -0.5).to(**kw))
         self.lora_B = torch.nn.Parameter(torch.zeros(d_out, r, **kw))
 
+    def quantize_base(self) -> "LoRALinear":
+        """The base weight to 8 bits, in place; returns the layer."""
+        if self.weight is not None:
+            codes, scales = quantize_weight(self.weight.detach())
+            self.weight = None
+            self.register_buffer("weight_codes", codes)
+            self.register_buffer("weight_scales", scales)
+        return self
+
+    def base_weight(self) -> torch.Tensor:
+        """The base weight's values in bf16."""
+        return self.weight if self.weight is not None else dequantize_weight(self.weight_codes, self.weight_scales)
+
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.d_in)
-        if torch.is_grad_enabled() and (x.requires_grad or self.lora_A.requires_grad or self.lora_B.requires_grad):
+        p = self.dropout if self.training else 0.0
+        if p > 0 or self.weight is None:
+            rng = torch.randint(0, 2 ** 62, (2,), dtype=torch.int64, device=x.device) if p > 0 else None
+            codes = self.weight is None
+            y, _ = torch.ops.lora_b200.lora_linear_adapter(
+                x2, self.weight_codes if codes else self.weight, self.weight_scales if codes else None, self.lora_A,
+                self.lora_B, self.scale, p, rng)
+        elif torch.is_grad_enabled() and (x.requires_grad or self.lora_A.requires_grad or self.lora_B.requires_grad):
             # keep T for the backward (it then reads X once less)
             y, _ = torch.ops.lora_b200.lora_linear_train(x2, self.weight, self.lora_A, self.lora_B, self.scale)
         else:
@@ -216,4 +372,5 @@ class LoRALinear(torch.nn.Module):
         return y.reshape(*lead, self.d_out)
 
     def extra_repr(self) -> str:
-        return f"d_in={self.d_in}, d_out={self.d_out}, r={self.r}, scale={self.scale:g}"
+        more = (f", dropout={self.dropout:g}" if self.dropout else "") + (", base=e4m3" if self.weight is None else "")
+        return f"d_in={self.d_in}, d_out={self.d_out}, r={self.r}, scale={self.scale:g}{more}"

@@ -1,0 +1,269 @@
+"""Dropout and the 8-bit base through the torch operators and LoRALinear:
+values and gradients against the 64-bit reference and against differences,
+stacked layers in a training step, eval mode, repeatability, checkpointing,
+capture, torch.compile, strides."""
+import numpy as np
+import pytest
+import torch
+from torch.utils.checkpoint import checkpoint
+
+import adapter_reference as R
+from test_gpu_adapter_dropout import BF16, host, make, rng_tensor
+from test_gpu_fp8 import values
+
+pytestmark = pytest.mark.gpu
+
+
+def layer(d_in, d_out, r, p, fp8, seed=0):
+    from lora_linear_layer_b200 import ops
+    g = torch.Generator().manual_seed(seed)
+    m = ops.LoRALinear(d_in, d_out, r, 2.0 * r, device="cuda", generator=g, dropout=p)
+    with torch.no_grad():
+        m.lora_B.copy_((torch.randn(d_out, r, generator=g) * 0.05).to(BF16))
+    return m.quantize_base() if fp8 else m
+
+
+def base_values(m):
+    return R.f64(m.weight) if m.weight is not None else values(m.weight_codes, m.weight_scales)
+
+
+def reference(m, x, dy, rng):
+    p = m.dropout if rng is not None else 0.0
+    mask = R.keep_mask(int(rng[0]), int(rng[1]), x.shape[0], m.d_in, p) if rng is not None else None
+    return R.layer(R.f64(x), base_values(m), R.f64(m.lora_A), R.f64(m.lora_B), m.scale, dY=R.f64(dy), mask=mask, p=p,
+                   fp8=m.weight is None)
+
+
+def draw():
+    """What the module draws next from torch's generator of the device."""
+    return torch.randint(0, 2 ** 62, (2,), dtype=torch.int64, device="cuda").cpu()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("p", [0.0, 0.2])
+def test_module_values_and_gradients(gpu, fp8, p):
+    m = layer(528, 272, 24, p, fp8)
+    x0 = make(3 * 100, 528, 272, 24)["X"].cuda()
+    dy = make(3 * 100, 528, 272, 24, seed=5)["dY"].cuda()
+    x = x0.reshape(3, 100, 528).clone().requires_grad_(True)
+    torch.manual_seed(11)
+    rng = draw() if p > 0 else None
+    torch.manual_seed(11)
+    y = m(x)
+    y.backward(dy.reshape(3, 100, 272))
+    ref = reference(m, x0, dy, rng)
+    for name, got in (("Y", y.reshape(-1, 272)), ("dX", x.grad.reshape(-1, 528)), ("dA", m.lora_A.grad),
+                      ("dB", m.lora_B.grad)):
+        R.check(name, host(got.detach()), ref[name])
+
+
+def test_eval_mode_is_the_plain_layer(gpu):
+    m = layer(264, 520, 16, 0.5, False).eval()
+    x = make(70, 264, 520, 16)["X"].cuda()
+    with torch.no_grad():
+        want = torch.ops.lora_b200.lora_linear(x, m.weight, m.lora_A, m.lora_B, m.scale)
+        assert torch.equal(m(x), want)
+
+
+def test_quantize_base_keeps_the_weights_values(gpu):
+    m = layer(272, 400, 8, 0.0, False)
+    w = R.f64(m.weight)
+    m.quantize_base()
+    assert m.weight is None and "weight_codes" in m.state_dict()
+    want = R.quantize(w, 128)[0]
+    np.testing.assert_array_equal(base_values(m), want)
+    np.testing.assert_array_equal(R.f64(m.base_weight()), want)
+    assert m.quantize_base() is m
+
+
+def test_two_layers_in_a_training_step(gpu):
+    """Quantise, then two steps of an up- and a down-projection with dropout:
+    every layer's output and gradients against the reference on the inputs
+    that it really had."""
+    up, down = layer(256, 640, 16, 0.1, True, seed=1), layer(640, 256, 16, 0.1, True, seed=2)
+    opt = torch.optim.SGD([q for m in (up, down) for q in m.parameters() if q.requires_grad], lr=1e-3)
+    seen = {}
+    for step in range(2):
+        opt.zero_grad(set_to_none=True)
+        x = make(333, 256, 640, 16, seed=step)["X"].cuda().requires_grad_(True)
+        torch.manual_seed(100 + step)
+        rngs = [draw(), draw()]
+        torch.manual_seed(100 + step)
+        h = up(x)
+        h.retain_grad()
+        a = torch.nn.functional.gelu(h)
+        a.retain_grad()
+        y = down(a)
+        dy = make(333, 640, 256, 16, seed=step)["dY"].cuda()
+        before = [[q.detach().clone() for q in (m.lora_A, m.lora_B)] for m in (up, down)]
+        y.backward(dy)
+        for m, xin, out, g_out, g_in, rng in ((down, a, y, dy, a.grad, rngs[1]), (up, x, h, h.grad, x.grad, rngs[0])):
+            ref = reference(m, xin.detach(), g_out, rng)
+            for name, got in (("Y", out), ("dX", g_in), ("dA", m.lora_A.grad), ("dB", m.lora_B.grad)):
+                R.check(name, host(got.detach()), ref[name])
+        opt.step()
+        seen[step] = before
+    assert not torch.equal(seen[0][0][0], seen[1][0][0])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_gradients_against_differences(gpu, fp8):
+    """The layer is linear in A, and in B: <dY, Y(A + D) - Y(A - D)> / 2 is
+    <dA, D>, up to the bounds of the four results.  Over a bf16 base it is
+    linear in X too."""
+    M, K, N, r, s, p = 200, 512, 384, 16, 1.0, 0.3
+    t = make(M, K, N, r)
+    from lora_linear_layer_b200 import ops
+    d = {k: v.cuda() for k, v in t.items()}
+    W, Ws = ops.quantize_weight(d["W"]) if fp8 else (d["W"], None)
+    Wv = values(W, Ws) if fp8 else R.f64(W)
+    rng = rng_tensor(4, 4)
+    mask = R.keep_mask(4, 4, M, K, p)
+
+    def forward(X, A, B):
+        Y = torch.ops.lora_b200.lora_linear_adapter(X, W, Ws, A, B, s, p, rng)[0]
+        bound = R.layer(R.f64(X), Wv, R.f64(A), R.f64(B), s, mask=mask, p=p, fp8=fp8)["Y"][1]
+        return host(Y), bound
+
+    Y, saved = torch.ops.lora_b200.lora_linear_adapter(d["X"], W, Ws, d["A"], d["B"], s, p, rng)
+    grads = dict(zip("XAB", torch.ops.lora_b200.lora_linear_adapter_bwd(d["X"], W, Ws, d["A"], d["B"], d["dY"], saved,
+                                                                        s, p, rng, True)))
+    bounds = R.layer(R.f64(t["X"]), Wv, R.f64(t["A"]), R.f64(t["B"]), s, dY=R.f64(t["dY"]), mask=mask, p=p, fp8=fp8)
+    dY = R.f64(t["dY"])
+    g = torch.Generator().manual_seed(1)
+    for name in ("A", "B") if fp8 else ("A", "B", "X"):
+        here = t[name].float()
+        # (the two points are rounded to bf16; being linear, the difference asks
+        # only for the step between them)
+        D = torch.randint(-3, 4, here.shape, generator=g) * torch.exp2(torch.floor(torch.log2(here.abs().clamp_min(
+            1e-6))) - 4)
+        hi, lo = (here + D).to(BF16), (here - D).to(BF16)
+        step = (R.f64(hi) - R.f64(lo)) / 2
+        (yh, bh), (yl, bl) = (forward(*(v.cuda() if n == name else d[n] for n in "XAB")) for v in (hi, lo))
+        got = (dY * (yh - yl)).sum() / 2
+        want = (host(grads[name]) * step).sum()
+        slack = (np.abs(dY) * (bh + bl)).sum() / 2 + (bounds["d" + name][1] * np.abs(step)).sum()
+        assert abs(got - want) <= slack, (name, got, want, slack)
+
+
+def test_same_seed_same_run_and_checkpointing(gpu):
+    m = layer(256, 384, 16, 0.3, True)
+    x0 = make(150, 256, 384, 16)["X"].cuda()
+    dy = make(150, 256, 384, 16)["dY"].cuda()
+
+    def go(call):
+        torch.manual_seed(3)
+        m.zero_grad(set_to_none=True)
+        x = x0.clone().requires_grad_(True)
+        y = call(x)
+        torch.rand(5, device="cuda")  # something else draws in between
+        y.backward(dy)
+        return y.detach(), x.grad, m.lora_A.grad, m.lora_B.grad
+
+    first = go(m)
+    for other in (go(m), go(lambda x: checkpoint(m, x, use_reentrant=False))):
+        for a, b in zip(first, other):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_captured_training_step_draws_new_masks(gpu, fp8):
+    m = layer(256, 384, 16, 0.5, fp8)
+    x = make(130, 256, 384, 16)["X"].cuda().requires_grad_(True)
+    dy = make(130, 256, 384, 16)["dY"].cuda()
+    args = (m.weight if m.weight is not None else m.weight_codes, None if m.weight is not None else m.weight_scales)
+
+    def step():
+        rng = torch.randint(0, 2 ** 62, (2,), dtype=torch.int64, device="cuda")
+        y, _ = torch.ops.lora_b200.lora_linear_adapter(x, *args, m.lora_A, m.lora_B, m.scale, 0.5, rng)
+        grads = torch.autograd.grad(y, (x, m.lora_A, m.lora_B), dy)
+        return (rng, y.detach(), *grads)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()  # no eager graph of these leaves is alive at capture
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    masks = []
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        rng = out[0].cpu()
+        ref = reference(m, x.detach(), dy, rng)
+        for name, got in zip(("Y", "dX", "dA", "dB"), out[1:]):
+            R.check(name, host(got), ref[name])
+        masks.append(tuple(rng.tolist()))
+    assert masks[0] != masks[1]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_compiled_fullgraph_equals_eager(gpu, fp8):
+    m = layer(512, 256, 16, 0.1, fp8)
+    x0 = make(96, 512, 256, 16)["X"].cuda()
+    dy = make(96, 512, 256, 16)["dY"].cuda()
+
+    def go(mod):
+        torch.manual_seed(8)
+        m.zero_grad(set_to_none=True)
+        x = x0.clone().requires_grad_(True)
+        y = mod(x)
+        y.backward(dy)
+        return y.detach(), x.grad, m.lora_A.grad, m.lora_B.grad
+
+    eager = go(m)
+    torch._dynamo.reset()
+    for a, b in zip(eager, go(torch.compile(m, backend="eager", fullgraph=True))):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_opcheck(gpu, fp8):
+    from lora_linear_layer_b200 import ops
+    t = {k: v.cuda() for k, v in make(40, 64, 48, 8).items()}
+    W, Ws = ops.quantize_weight(t["W"]) if fp8 else (t["W"], None)
+    X, A, B = (t[k].requires_grad_(True) for k in ("X", "A", "B"))
+    torch.library.opcheck(torch.ops.lora_b200.lora_linear_adapter.default, (X, W, Ws, A, B, 1.0, 0.1, rng_tensor(1, 2)),
+                          # (the schema test does arithmetic on its inputs, which torch lacks for e4m3)
+                          test_utils=(() if fp8 else ("test_schema",)) + ("test_faketensor", "test_autograd_registration"))
+
+
+def test_strided_and_shared_inputs(gpu):
+    """A transposed input, a gradient that is a broadcast, and one adapter
+    used twice in a graph (its gradients add up)."""
+    m = layer(256, 256, 8, 0.25, True)
+    x = make(96, 256, 256, 8)["X"].cuda()
+    xt = x.t().contiguous().t()
+    assert not xt.is_contiguous()
+    torch.manual_seed(1)
+    a = m(x)
+    torch.manual_seed(1)
+    assert torch.equal(a, m(xt))
+    torch.manual_seed(2)
+    rngs = [draw(), draw()]
+    torch.manual_seed(2)
+    y1 = m(x)
+    y2 = m(y1.detach())
+    (y1.sum() + y2.sum()).backward()  # the gradients of a sum are an expanded one
+    ones = torch.ones(96, 256, dtype=BF16)
+    r1, r2 = reference(m, x, ones, rngs[0]), reference(m, y1.detach(), ones, rngs[1])
+    for name, got in (("dA", m.lora_A.grad), ("dB", m.lora_B.grad)):
+        v = r1[name][0] + r2[name][0]
+        bound = r1[name][1] + r2[name][1] + R.HALF_BF16 * (np.abs(v) + r1[name][1] + r2[name][1])
+        R.check(name, host(got), (v, bound))
+
+
+def test_tensors_of_a_call_share_a_device(gpu):
+    t = {k: v.cuda() for k, v in make(8, 64, 64, 8).items()}
+    Y = torch.empty(8, 64, dtype=BF16, device="cuda")
+    ws = torch.empty(gpu.lora_bwd_workspace_size(8, 64, 64, 8), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        gpu.lora_fwd_dropout(t["X"], t["W"], t["A"].cpu(), t["B"], Y, 1.0, 0.1, rng_tensor(0, 0), ws)
+    with pytest.raises(ValueError):
+        gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, 1.0, 0.1, rng_tensor(0, 0).cpu(), ws)
+    with pytest.raises(ValueError):
+        gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y.t(), 1.0, 0.1, rng_tensor(0, 0), ws)
+    with pytest.raises(gpu.LoraError):
+        gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, 1.0, 0.1, rng_tensor(0, 0), ws[:256])
