@@ -15,7 +15,7 @@
 // What bounds it is the read of P (and the write of its codes).  So P comes
 // by TMA as in the plain product, several stages ahead, and eight warps work
 // on each stage in shared memory between the copy and the MMA: they take the
-// maximum of a row's 128 values over 8 lanes, write the codes to global
+// maximum of a row's 128 values over 4 lanes, write the codes to global
 // memory, and put the masked values back where the MMA reads them (a dropped
 // value is set to zero by a select, so the product needs no mask and a
 // dropped infinity or NaN is gone; 1/(1-p) is in the scale).  The mask is
@@ -228,73 +228,104 @@ __global__ void __launch_bounds__(pass_threads(RCW, P_MN), pass_workers(RCW, P_M
     if (drop) ds = drop_load(a.drop);
     int stage = 0;
     uint32_t phase = 0;
-    const int c = lane & 7, r4 = lane >> 3;
-    // Addresses inside a stage: a lane's 16-byte chunk of rows w * kRows + r4
-    // and four rows on (the swizzle repeats every 8 rows).
-    //  K-major: four rows at a time, 8 lanes a row, 16 consecutive values a
-    //  lane: sub-stage c / 4, chunks 2 (c % 4) and the next.  The lanes of
-    //  the second sub-stage take theirs in the other order, so that the 8
-    //  lanes of a row touch 8 different bank groups.
-    //  MN-major: 128 (column chunk of 64, token) rows, 8 lanes a row.
+    // What bounds these warps is their instructions (at 8 lanes a row and one
+    // address calculation a store X[32768, 4096] took 88 us rounded and 75 us
+    // masked, against 48 us untouched), so a lane takes as much of a row as it
+    // can, and pointers run along.
     constexpr int kRows = 128 / kPassWorkers;
-    const uint32_t odd = P_MN ? 0u : uint32_t(c >> 2);
-    uint32_t off[2];
+    if constexpr (!P_MN) {
+      // Eight rows at a time, 4 lanes a row, 32 consecutive values a lane: four
+      // 16-byte chunks of sub-stage c / 2.  The lanes of the second sub-stage
+      // take theirs in the order 2, 3, 0, 1: then the 8 lanes of two rows touch
+      // 8 different bank groups (the swizzle gives the other two bits).
+      constexpr int kIts = kRows / 8;
+      const int c = lane & 3, r8 = lane >> 2;
+      const int row0 = i0 + w * kRows + r8;
+      const uint32_t flip = uint32_t(c >> 1) * 2u;
+      const uint32_t row_at = uint32_t(c >> 1) * L.sub_bytes + uint32_t(w * kRows + r8) * 128u;
+      uint32_t at[4];  // inside a stage, of a lane's chunks 0 ^ flip, 1 ^ flip, ...
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t row = uint32_t(w * kRows + 4 * i + r4);
-      off[i] = P_MN ? (row >> 6) * 8192u + swz_offset(row & 63u, uint32_t(c), 128u)
-                    : odd * L.sub_bytes + swz_offset(row, uint32_t(c & 3) * 2u + odd, 128u);
-    }
-    const int row0 = P_MN ? (w * kRows + r4) & 63 : i0 + w * kRows + r4;  // token in the stage, or row of P
-    const uint32_t c8_mn = uint32_t(i0 + (w * kRows >> 6) * 64) / 8u + uint32_t(c);
-    const bool any = P_MN || i0 + w * kRows < a.rows;  // (rows past the end are zero fill)
-    const int row_blocks = (a.rows + 127) / 128;
-    const size_t code0 = size_t(row0) * size_t(a.K) + size_t(c * 16);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!warp_wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL)) break;
-      const uint32_t st = sbase + uint32_t(stage) * L.stage_bytes;
-      if constexpr (!P_MN) {
+      for (uint32_t j = 0; j < 4; ++j) at[j] = row_at + ((uint32_t(c & 1) * 4u + (j ^ flip)) ^ uint32_t(r8)) * 16u;
+      const bool any = i0 + w * kRows < a.rows;  // (rows past the end are zero fill)
+      uint8_t* code = QUANT ? a.codes + size_t(row0) * size_t(a.K) + size_t(kb0) * 128 + size_t(c * 32) : nullptr;
+      const size_t code_step = size_t(8) * size_t(a.K);
+      const int row_blocks = (a.rows + 127) / 128;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL)) break;
         if (any) {
-          const int k = kb * 128 + c * 16;
+          const uint32_t st = sbase + uint32_t(stage) * L.stage_bytes;
+          const int k = kb * 128 + c * 32;
+          uint4 v[kIts][4];
 #pragma unroll
-          for (int it = 0; it < kRows / 4; ++it) {
-            // chunk 2 (c % 4) + odd, and the other of the two
-            const uint32_t at0 = st + off[it & 1] + uint32_t(it >> 1) * 1024u, at1 = at0 ^ 16u;
-            const uint4 v0 = ld_shared_v4(at0), v1 = ld_shared_v4(at1);
-            const int gi = row0 + 4 * it;
-            if constexpr (QUANT) {
-              uint32_t m = amax_bf16x16(v0, v1);
+          for (int it = 0; it < kIts; ++it)
 #pragma unroll
-              for (int s = 4; s > 0; s >>= 1) m = amax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, s));
-              const uint32_t b = e8m0_of_pair(m), f = e8m0_inverse(b);
-              const uint2 q0 = quant8(v0, f), q1 = quant8(v1, f);
-              if (gi < a.rows) {
-                if (k < a.K)
-                  *reinterpret_cast<uint4*>(a.codes + code0 + size_t(4 * it) * size_t(a.K) + size_t(kb) * 128) =
-                      odd ? make_uint4(q1.x, q1.y, q0.x, q0.y) : make_uint4(q0.x, q0.y, q1.x, q1.y);
-                if (c == 0)
-                  a.scales[scale_atom_offset(gi, kb, row_blocks)] = uint8_t(b);
+            for (int j = 0; j < 4; ++j) v[it][j] = ld_shared_v4(st + at[j] + uint32_t(it) * 1024u);
+          if constexpr (QUANT) {
+            uint8_t* const scale = a.scales + scale_atom_offset(row0, kb, row_blocks);  // 8 rows on: 128 bytes on
+            uint32_t m[kIts];
+#pragma unroll
+            for (int it = 0; it < kIts; ++it)
+              m[it] = amax_bf16x2(amax_bf16x16(v[it][0], v[it][1]), amax_bf16x16(v[it][2], v[it][3]));
+#pragma unroll
+            for (int s = 2; s > 0; s >>= 1)
+#pragma unroll
+              for (int it = 0; it < kIts; ++it) m[it] = amax_bf16x2(m[it], __shfl_xor_sync(0xffffffffu, m[it], s));
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+              const uint32_t b = e8m0_of_pair(m[it]), f = e8m0_inverse(b);
+              const uint2 q0 = quant8(v[it][0], f), q1 = quant8(v[it][1], f);
+              const uint2 q2 = quant8(v[it][2], f), q3 = quant8(v[it][3], f);
+              if (row0 + 8 * it < a.rows) {
+                uint8_t* const dst = code + size_t(it) * code_step;
+                // (K is a multiple of 16)
+                if (k + int(flip) * 8 < a.K) *reinterpret_cast<uint4*>(dst + flip * 8u) = make_uint4(q0.x, q0.y, q1.x, q1.y);
+                if (k + 16 - int(flip) * 8 < a.K)
+                  *reinterpret_cast<uint4*>(dst + 16u - flip * 8u) = make_uint4(q2.x, q2.y, q3.x, q3.y);
+                if (c == 0) scale[it * 128] = uint8_t(b);
               }
             }
-            if (drop) {
-              const uint32_t c8 = uint32_t(k) >> 3;
-              st_shared_v4(at0, drop_bf16x8(v0, drop_block(ds, c8 + odd, uint32_t(gi)), ds.thr_hi));
-              st_shared_v4(at1, drop_bf16x8(v1, drop_block(ds, c8 + (odd ^ 1u), uint32_t(gi)), ds.thr_hi));
-            }
+            code += 128;
+          }
+          if (drop) {
+            const uint32_t c8 = uint32_t(k) >> 3;
+#pragma unroll
+            for (int it = 0; it < kIts; ++it)
+#pragma unroll
+              for (uint32_t j = 0; j < 4; ++j)
+                st_shared_v4(st + at[j] + uint32_t(it) * 1024u,
+                             drop_bf16x8(v[it][j], drop_block(ds, c8 + (j ^ flip), uint32_t(row0 + 8 * it)), ds.thr_hi));
           }
         }
-      } else {
+        if (drop) fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready_bar(stage));
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+    } else {
+      // 64 tokens x two chunks of 64 columns: 128 rows of 8 lanes, four at a time
+      const int c = lane & 7, r4 = lane >> 3;
+      uint32_t off[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t row = uint32_t(w * kRows + 4 * i + r4);
+        off[i] = (row >> 6) * 8192u + swz_offset(row & 63u, uint32_t(c), 128u);
+      }
+      const int tok0 = (w * kRows + r4) & 63;
+      const uint32_t c8 = uint32_t(i0 + (w * kRows >> 6) * 64) / 8u + uint32_t(c);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL)) break;
+        const uint32_t st = sbase + uint32_t(stage) * L.stage_bytes;
 #pragma unroll
         for (int it = 0; it < kRows / 4; ++it) {
           const uint32_t addr = st + off[it & 1] + uint32_t(it >> 1) * 1024u;
-          const uint32_t tok = uint32_t(kb * 64 + row0 + 4 * it);
-          st_shared_v4(addr, drop_bf16x8(ld_shared_v4(addr), drop_block(ds, c8_mn, tok), ds.thr_hi));
+          const uint32_t tok = uint32_t(kb * 64 + tok0 + 4 * it);
+          st_shared_v4(addr, drop_bf16x8(ld_shared_v4(addr), drop_block(ds, c8, tok), ds.thr_hi));
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready_bar(stage));
+        if (++stage == S) { stage = 0; phase ^= 1u; }
       }
-      if (drop) fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ready_bar(stage));
-      if (++stage == S) { stage = 0; phase ^= 1u; }
     }
   }
 

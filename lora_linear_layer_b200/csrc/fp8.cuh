@@ -44,9 +44,8 @@ __device__ __forceinline__ uint32_t amax_bf16x16(uint4 x, uint4 y) {
 // 31 carries exactly then.  A subnormal bf16 (x < -126) is below
 // 448 * 2^-127 in any case.
 __device__ __forceinline__ uint32_t e8m0_of_amax(uint32_t amax_bits) {
-  if (amax_bits >= 0x7F80u) return 255u;
-  if (amax_bits == 0u) return 127u;
-  return uint32_t(max(int((amax_bits + 31u) >> 7) - 8, 0));
+  const uint32_t b = uint32_t(max(int((amax_bits + 31u) >> 7) - 8, 0));
+  return amax_bits >= 0x7F80u ? 255u : amax_bits == 0u ? 127u : b;  // (selects: a branch costs more)
 }
 
 // The same for the larger of two packed magnitudes (signs are ignored).
