@@ -84,9 +84,9 @@ void pick_pass(int64_t rows, int64_t K, int r, bool p_mn, bool r_mn, int out_mod
   const int block_k = p_mn ? 64 : 128;
   const int nb = int((K + block_k - 1) / block_k);
   const int tiles = int(std::max<int64_t>(1, launch_tiles));
-  // (one block an SM: clusters of 8 leave SMs of a GPC idle, so that 17 row
-  // tiles took two rounds, 28 us on X[2051, 2560] at r = 128)
-  const int most = per_sm == 1 ? 4 : 8;
+  // (one block an SM: two clusters of 8 fit a GPC, so that 17 row tiles took
+  // two rounds, 28 us on X[2051, 2560] at r = 128 against 17 us in fours)
+  const int most = per_sm == 1 && tiles > 14 ? 4 : 8;
   int splits = std::max(1, std::min({per_sm * sm_count / tiles, most, std::max(1, nb * block_k / 256)}));
   a.nb_per_split = std::max(1, (nb + splits - 1) / splits);
   splits = std::max(1, (nb + a.nb_per_split - 1) / a.nb_per_split);
@@ -312,70 +312,111 @@ lora_status_t launch_dx(const void* dY, const Rounded& q, const Base& W, const v
 // rows, which costs less than the pass's long prologue and few blocks up to
 // M * r_pad = 8192 (X[512, 8192] at r = 16: 14 against 18 us; at M = 1024 they
 // tie, and X[512, 4096] at r = 128 takes 29 against 17 us).
-bool use_prep(int64_t M, int32_t r, const DropArgs& drop) { return drop.rng == nullptr && M * r_pad_of(r) <= 8192; }
+bool use_prep(int64_t M, int32_t r) { return M * r_pad_of(r) <= 8192; }
 
-// T and the codes of X for few tokens, without dropout.
+// T and, with `q`, the codes of X for few tokens.
 lora_status_t launch_prep(const void* X, const void* A, int64_t M, int64_t d_in, int32_t r, float scale,
-                          __nv_bfloat16* Tws, const Rounded& q, cudaStream_t st) {
+                          const DropArgs& drop, __nv_bfloat16* Tws, const Rounded* q, cudaStream_t st) {
   PrepArgs p;
+  std::memset(&p, 0, sizeof(p));
   p.X = reinterpret_cast<const uint8_t*>(X);
   p.A = reinterpret_cast<const uint8_t*>(A);
   p.T = Tws;
-  p.codes = q.codes;
-  p.scales = q.scales;
-  p.atoms = q.atoms;
+  p.drop = drop;
   p.M = int32_t(M);
   p.K = int32_t(d_in);
   p.r = r;
   p.r_pad = r_pad_of(r);
   p.t_blocks = kPrepSplits * (p.r_pad / kPrepRanks) * ((p.M + kPrepTokens - 1) / kPrepTokens);
-  p.scale = scale;
+  p.scale = scale * drop.inv_keep;
   auto blocks = [](int64_t items) {  // whole clusters of blocks, a warp an item
     return (items + kPrepWarps * kPrepSplits - 1) / (kPrepWarps * kPrepSplits) * kPrepSplits;
   };
-  p.q_blocks = int32_t(blocks(M * ((d_in + 511) / 512)));
-  const int64_t a_blocks = q.atoms.bytes != nullptr ? blocks(int64_t(q.atoms.tiles) * q.atoms.groups * 2) : 0;
+  int64_t a_blocks = 0;
+  if (q != nullptr) {
+    p.codes = q->codes;
+    p.scales = q->scales;
+    p.atoms = q->atoms;
+    p.q_blocks = int32_t(blocks(M * ((d_in + 511) / 512)));
+    if (q->atoms.bytes != nullptr) a_blocks = blocks(int64_t(q->atoms.tiles) * q->atoms.groups * 2);
+  }
   const unsigned grid = unsigned(p.t_blocks + p.q_blocks + a_blocks);
   const dim3 cl(kPrepSplits, 1, 1);
   return launch_ex("token prep", token_prep_kernel, dim3(grid), dim3(kPrepThreads), 0, st, &cl, p);
 }
 
-// Y over an 8-bit base for at most kStreamMax tokens from what launch_prep
-// left.
-lora_status_t launch_stream(const Base& W, const void* B, void* Y, int64_t M, int64_t d_in, int64_t d_out, int32_t r,
-                            const __nv_bfloat16* Tws, const uint8_t* codes, const uint8_t* scales, int sm_count,
-                            cudaStream_t st) {
+template <bool FP8, bool MN, bool DROP>
+lora_status_t launch_stream_t(const CUtensorMap* maps, const StreamArgs& a, int tiles, uint32_t smem, cudaStream_t st) {
+  auto kern = token_stream_kernel<FP8, MN, DROP>;
+  if (!ensure_smem_attr(kern, smem)) return LORA_ERR_CUDA;
+  const dim3 cl(1, unsigned(a.splits), 1);
+  return launch_ex("token stream", kern, dim3(unsigned(tiles), unsigned(a.splits)), dim3(kStreamThreads), smem, st, &cl,
+                   maps[0], maps[1], maps[2], maps[3], a);
+}
+
+// Few enough tokens for launch_stream (`drop`: the product masks its rank
+// side).  Above 128 tokens its blocks' way out, 128 rows by every token, costs
+// as much as a short contraction (X[223, 288], N = 1664 at 8 bits: 21 us
+// against 9 us by tiles; [256, 4096], N = 4096: 22 against 17 us), and it
+// pays for splitting a long one alone ([256, 14336], N = 4096: 32 against 74).
+bool use_stream(int64_t M, int64_t K, bool drop) {
+  return M <= 128 || (M <= (drop ? kStreamMaxDrop : kStreamMax) && K > 6144);
+}
+
+// Y (mn = false, from T in `U`) or dX (mn = true, from dT in `U`) for few
+// tokens; `in` is X or dY.
+lora_status_t launch_stream(bool mn, const void* in, const Rounded& q, const Base& W, const void* V, void* out,
+                            const __nv_bfloat16* U, int64_t M, int64_t d_in, int64_t d_out, int32_t r,
+                            const DropArgs& drop, int sm_count, cudaStream_t st) {
+  const bool fp8 = W.fp8(), masked = mn && drop.rng != nullptr;
+  const int64_t N = mn ? d_in : d_out, K = mn ? d_out : d_in;
   StreamArgs a;
-  a.Ws = reinterpret_cast<const uint8_t*>(W.scales);
-  a.x_scales = reinterpret_cast<const uint32_t*>(scales);
-  a.Y = reinterpret_cast<__nv_bfloat16*>(Y);
+  std::memset(&a, 0, sizeof(a));
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.M = int32_t(M);
-  a.N = int32_t(d_out);
-  a.K = int32_t(d_in);
+  a.N = int32_t(N);
+  a.K = int32_t(K);
   a.r_pad = r_pad_of(r);
   a.tok_pad = (a.M + 15) / 16 * 16;
+  a.drop = masked ? drop : DropArgs{nullptr, 0u, 1.0f};
+  if (fp8) {
+    a.w_scales = reinterpret_cast<const uint8_t*>(W.scales);
+    a.x_scales = reinterpret_cast<const uint32_t*>(q.scales);
+    a.ws_row = mn ? 1 : int32_t(qblocks(d_in));
+    a.ws_k = mn ? int32_t(qblocks(d_in)) : 1;
+  }
   const uint32_t stage = StreamLayout(a.tok_pad, 0).stage_bytes;
   const uint32_t fixed = kStreamScaleBufs * kStreamScaleBytes + 2048;
   // two blocks an SM where four stages fit in half of it
   const uint32_t half = kSmemPerSM / 2 - 1024 - fixed;
   a.stages = std::min(8, int((half / stage >= 4 ? half : kSmemMax - fixed) / stage));
   const uint32_t smem = StreamLayout(a.tok_pad, a.stages).total + 1024;
-  const int per_sm = std::max(1, std::min(int(kSmemPerSM / (smem + 1024)), int(512 / stream_tmem_cols(a.tok_pad))));
-  const int tiles = int((d_out + 127) / 128), nk = int((d_in + 127) / 128);
-  int splits = std::max(1, std::min({8, per_sm * sm_count / tiles, nk / 2}));
+  const int per_sm =
+      std::max(1, std::min(int(kSmemPerSM / (smem + 1024)), int(512 / stream_tmem_cols(a.tok_pad, masked))));
+  const int tiles = int((N + 127) / 128), block_k = fp8 ? 128 : 64, nk = int((K + block_k - 1) / block_k);
+  const int splits = std::max(1, std::min({8, per_sm * sm_count / tiles, nk / 2}));
   a.kb_per_split = (nk + splits - 1) / splits;
   a.splits = (nk + a.kb_per_split - 1) / a.kb_per_split;
   a.wait_limit_ns = kWaitLimitNs;
-  CUtensorMap mw, mx, mb, mt;
-  if (!make_map_u8(&mw, W.w, d_in, d_out, d_in, 128, 128) ||
-      !make_map_u8(&mx, codes, d_in, M, d_in, 128, uint32_t(a.tok_pad)) ||
-      !make_map(&mb, B, r, d_out, r, 64, 128, 128) ||
-      !make_map(&mt, Tws, uint64_t(a.r_pad), M, uint64_t(a.r_pad), 64, uint32_t(a.tok_pad), 128))
-    return LORA_ERR_CUDA;
-  if (!ensure_smem_attr(token_stream_kernel, smem)) return LORA_ERR_CUDA;
-  const dim3 cl(1, unsigned(a.splits), 1);
-  return launch_ex("token stream", token_stream_kernel, dim3(unsigned(tiles), unsigned(a.splits)),
-                   dim3(kStreamThreads), smem, st, &cl, mw, mx, mb, mt, a);
+  const uint32_t box_m = uint32_t(a.tok_pad);
+  CUtensorMap maps[4];
+  bool ok;
+  if (fp8)  // (128 codes x 128 rows either way)
+    ok = make_map_u8(&maps[0], W.w, d_in, d_out, d_in, 128, 128) && make_map_u8(&maps[1], q.codes, K, M, K, 128, box_m);
+  else
+    ok = make_map(&maps[0], W.w, d_in, d_out, d_in, 64, mn ? 64 : 128, 128) &&
+         make_map(&maps[1], in, K, M, K, 64, box_m, 128);
+  ok = ok && (mn ? make_map(&maps[2], V, d_in, r, d_in, 64, 64, 128) : make_map(&maps[2], V, r, d_out, r, 64, 128, 128)) &&
+       make_map(&maps[3], U, uint64_t(a.r_pad), M, uint64_t(a.r_pad), 64, box_m, 128);
+  if (!ok) return LORA_ERR_CUDA;
+  if (masked)
+    return fp8 ? launch_stream_t<true, true, true>(maps, a, tiles, smem, st)
+               : launch_stream_t<false, true, true>(maps, a, tiles, smem, st);
+  if (mn)
+    return fp8 ? launch_stream_t<true, true, false>(maps, a, tiles, smem, st)
+               : launch_stream_t<false, true, false>(maps, a, tiles, smem, st);
+  return fp8 ? launch_stream_t<true, false, false>(maps, a, tiles, smem, st)
+             : launch_stream_t<false, false, false>(maps, a, tiles, smem, st);
 }
 
 // --------------------------------------------------------- whole layers ----
@@ -384,7 +425,7 @@ lora_status_t launch_stream(const Base& W, const void* B, void* Y, int64_t M, in
 lora_status_t launch_t_codes(const void* X, const void* A, int64_t M, int64_t d_in, int32_t r, float scale,
                              const DropArgs& drop, __nv_bfloat16* Tws, const Rounded* q, int sm_count,
                              cudaStream_t st) {
-  if (q != nullptr && use_prep(M, r, drop)) return launch_prep(X, A, M, d_in, r, scale, Tws, *q, st);
+  if (use_prep(M, r)) return launch_prep(X, A, M, d_in, r, scale, drop, Tws, q, st);
   return launch_down(X, A, M, d_in, r, scale, drop, Tws, q, sm_count, st);
 }
 
@@ -411,13 +452,13 @@ lora_status_t adapter_fwd_run(const void* X, const Base& W, const void* A, const
   lora_status_t s = device_info(dev);
   if (s != LORA_OK || M == 0) return s;
   const int sms = dev.sm_count;
-  const bool fp8 = W.fp8(), stream = fp8 && M <= kStreamMax;
+  const bool fp8 = W.fp8(), stream = use_stream(M, d_in, false);
   Places at(workspace, M, d_in, d_out, r);
   LrCfg c;
   if (!stream) pick_lr(M, d_out, d_in, r, fp8, false, sms, c);
   if (fp8 && !stream) at.q.atoms = scale_atom_args(W, at.q, c, false, d_in, d_out);
   if ((s = launch_t_codes(X, A, M, d_in, r, scale, drop, at.T, fp8 ? &at.q : nullptr, sms, st)) != LORA_OK) return s;
-  if (stream) return launch_stream(W, B, Y, M, d_in, d_out, r, at.T, at.q.codes, at.q.scales, sms, st);
+  if (stream) return launch_stream(false, X, at.q, W, B, Y, at.T, M, d_in, d_out, r, drop, sms, st);
   c.args.f.out = reinterpret_cast<__nv_bfloat16*>(Y);
   return launch_up(X, at.q, W, B, Y, at.T, c, r, sms, st);
 }
@@ -449,10 +490,13 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
   if (!saved &&
       (s = launch_t_codes(X, A, M, d_in, r, scale, drop, at.T, fp8 ? &at.q : nullptr, sms, st)) != LORA_OK)
     return s;
+  const bool stream = use_stream(M, d_out, drop.rng != nullptr);
   LrCfg c;
-  pick_lr(M, d_in, d_out, r, fp8, true, sms, c);
-  c.args.f.out = reinterpret_cast<__nv_bfloat16*>(dX);
-  c.args.drop = drop;
+  if (!stream) {
+    pick_lr(M, d_in, d_out, r, fp8, true, sms, c);
+    c.args.f.out = reinterpret_cast<__nv_bfloat16*>(dX);
+    c.args.drop = drop;
+  }
   {
     PassCfg p;
     pick_pass(M, d_out, r, false, true, OUT_ROWS_RPAD, (M + 127) / 128, sms, p);
@@ -464,7 +508,7 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
     if (fp8) {
       p.args.codes = at.q.codes;
       p.args.scales = at.q.scales;
-      at.q.atoms = scale_atom_args(W, at.q, c, true, d_in, d_out);
+      if (!stream) at.q.atoms = scale_atom_args(W, at.q, c, true, d_in, d_out);
       s = launch_pass<false, true>(m, p, st, nullptr, nullptr, at.q.atoms);
     } else {
       s = launch_pass<false, false>(m, p, st);
@@ -494,6 +538,7 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
       return LORA_ERR_CUDA;
     if ((s = launch_pass<true, false>(ma, ca, st, &mb, &cb)) != LORA_OK) return s;
   }
+  if (stream) return launch_stream(true, dY, at.q, W, A, dX, at.dT, M, d_in, d_out, r, drop, sms, st);
   return launch_dx(dY, at.q, W, A, dX, at.dT, c, r, sms, st);
 }
 

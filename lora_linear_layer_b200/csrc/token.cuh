@@ -1,13 +1,16 @@
-// token.cuh - the layer over an 8-bit base for few tokens, without dropout:
-//     Y = Xq Wq^T + T B^T,   T = s X A^T
+// token.cuh - the layer for few tokens:
+//     Y  = X W^T + T B^T,                 T = s/(1-p) (m * X) A^T
+//     dX = dY W + m * (dT A)/(1-p)
+// over a bf16 base or an 8-bit one (Xq, dYq and Wq in the base product).
 //
-// At this size the layer is one read of the weight (d_out * d_in bytes) and
-// the latency around it.  Two launches:
-//  1. token_prep_kernel: T and the codes and scales of X, beside each other
-//     in one grid of small blocks that read straight into registers.
+// At this size the layer is one read of the weight and the latency around
+// it.  Two launches forward:
+//  1. token_prep_kernel: T, and with an 8-bit base the codes and scales of X,
+//     beside each other in one grid of small blocks that read straight into
+//     registers.
 //  2. token_stream_kernel: W streamed through the tensor pipe, with W's rows
-//     as the MMA's 128 rows and the tokens as its N columns, so that no row
-//     of a tile is empty and each W tile is read once.
+//     (columns for dX) as the MMA's 128 rows and the tokens as its N columns,
+//     so that no row of a tile is empty and each W tile is read once.
 // The second launch starts while the first runs (programmatic dependent
 // launch) and fetches its first stages of W before it waits: W was complete
 // before the first kernel began, since that one waits before it lets a
@@ -16,6 +19,7 @@
 
 #include "common.cuh"
 #include "fp8.cuh"
+#include "philox.cuh"
 
 namespace lora {
 
@@ -29,10 +33,11 @@ struct PrepArgs {
   const uint8_t* X;      // bf16 [M, K]
   const uint8_t* A;      // bf16 [r, K]
   __nv_bfloat16* T;      // [M, r_pad]
-  uint8_t* codes;        // [M, K]
+  uint8_t* codes;        // [M, K] (with an 8-bit base)
   uint8_t* scales;       // e8m0 bytes (scale_atom_offset)
   int32_t M, K, r, r_pad, t_blocks, q_blocks;
   float scale;
+  DropArgs drop;
   ScaleAtomArgs atoms;
 };
 
@@ -100,6 +105,9 @@ __global__ void __launch_bounds__(kPrepThreads) token_prep_kernel(const PrepArgs
     src[i] = a.X + size_t(imin(m0 + g + 8 * i, a.M - 1)) * size_t(a.K) * 2;
     src[2 + i] = a.A + size_t(imin(j0 + g + 8 * i, a.r - 1)) * size_t(a.K) * 2;
   }
+  const bool drop = a.drop.rng != nullptr;
+  DropState ds{};
+  if (drop) ds = drop_load(a.drop);
   float d[2][4] = {};
   constexpr int kUnroll = 4;
   constexpr int kStep = kPrepSplits * kPrepWarps * 32;
@@ -118,6 +126,14 @@ __global__ void __launch_bounds__(kPrepThreads) token_prep_kernel(const PrepArgs
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[u][i] = make_uint4(0, 0, 0, 0);
       }
+    if (drop) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v[u][i] = drop_bf16x8(v[u][i], drop_block(ds, uint32_t(k0 + u * kStep) / 8u + uint32_t(t), uint32_t(m0 + g + 8 * i)),
+                                ds.thr_hi);
+    }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
@@ -154,20 +170,25 @@ __global__ void __launch_bounds__(kPrepThreads) token_prep_kernel(const PrepArgs
 
 // The contraction of the second launch is split over a cluster whose fp32
 // partials are added in split order through distributed shared memory, as in
-// skinny.cuh; T B^T is one or two more K blocks of the first split.  The
-// scales go to TMEM as in lowrank_gemm.cuh; W's are one for the whole tile.
+// skinny.cuh; the rank product is one or two more K blocks of the first split.
+// The scales go to TMEM as in lowrank_gemm.cuh; W's are one for the whole
+// tile.  DROP (dX with a mask): the rank product has an accumulator of its
+// own, and the first split masks and adds it when it takes its partial out.
 constexpr int kStreamMax = 256;
+constexpr int kStreamMaxDrop = 192;  // two accumulators
 constexpr int kStreamThreads = 192;
 constexpr int kStreamScaleBufs = 4;
 constexpr uint32_t kStreamScaleBytes = 512u * 3u;
 
 struct StreamArgs {
-  const uint8_t* Ws;         // [ceil(N / 128), ceil(K / 128)]
-  const uint32_t* x_scales;  // words of 4 scale bytes (scale_atom_offset)
-  __nv_bfloat16* Y;          // [M, N]
+  const uint8_t* w_scales;   // 8-bit base: bytes of its blocks
+  int32_t ws_row, ws_k;      // strides along the MMA's rows and along K
+  const uint32_t* x_scales;  // 8-bit base: words of 4 scale bytes (scale_atom_offset)
+  __nv_bfloat16* out;        // [M, N]
   int32_t M, N, K, r_pad;
   int32_t tok_pad;           // tokens rounded up to 16 (UMMA N)
   int32_t stages, kb_per_split, splits;
+  DropArgs drop;
   uint64_t wait_limit_ns;
 };
 
@@ -184,14 +205,19 @@ struct StreamLayout {
   }
 };
 
-__host__ __device__ inline uint32_t stream_tmem_cols(int tok_pad) {
-  return tok_pad <= 64 ? 128u : tok_pad <= 192 ? 256u : 512u;
+// Accumulators and, in the last 64 columns, the scales.
+__host__ __device__ inline uint32_t stream_tmem_cols(int tok_pad, bool drop) {
+  const int need = tok_pad * (drop ? 2 : 1) + 16 * kStreamScaleBufs;
+  return need <= 128 ? 128u : need <= 256 ? 256u : 512u;
 }
 
+template <bool FP8, bool MN, bool DROP>
 __global__ void __launch_bounds__(kStreamThreads)
     token_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                        const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmT,
-                        const StreamArgs a) {
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmU,
+                        const __grid_constant__ StreamArgs a) {
+  static_assert(!DROP || MN, "only dX masks its rank product");
+  constexpr int kStageK = FP8 ? 128 : 64;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -208,7 +234,7 @@ __global__ void __launch_bounds__(kStreamThreads)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + L.off_bar + 8 * (2 * S + 2 + 2 * kStreamScaleBufs));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ncols = stream_tmem_cols(a.tok_pad);
+  const uint32_t ncols = stream_tmem_cols(a.tok_pad, DROP);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -224,8 +250,8 @@ __global__ void __launch_bounds__(kStreamThreads)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
-    tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmT);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmU);
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), ncols);
@@ -238,7 +264,7 @@ __global__ void __launch_bounds__(kStreamThreads)
 
   const int n0 = int(blockIdx.x) * 128;
   const int split = blockIdx.y;
-  const int nk = (a.K + 127) / 128;
+  const int nk = (a.K + kStageK - 1) / kStageK;
   const int kb0 = imin(nk, split * a.kb_per_split);
   const int nkb = imin(nk, kb0 + a.kb_per_split) - kb0;
   const int nr = split == 0 ? (a.r_pad + 63) / 64 : 0;  // rank blocks
@@ -246,15 +272,27 @@ __global__ void __launch_bounds__(kStreamThreads)
 
   if (warp == 0) {
     if (lane == 0) {
+      // the weight's 128 rows (columns with MN) of one K block into a stage
+      auto load_w = [&](uint32_t st, uint32_t fb, int kb) {
+        const int k0 = kb * kStageK;
+        if constexpr (!MN) {
+          tma_load_2d(st, &tmW, fb, k0, n0);
+        } else if constexpr (FP8) {
+          tma_load_2d(st, &tmW, fb, n0, k0);
+        } else {
+          tma_load_2d(st, &tmW, fb, n0, k0);
+          tma_load_2d(st + 8192u, &tmW, fb, n0 + 64, k0);
+        }
+      };
       const int pre = imin(S, nkb);
       for (int i = 0; i < pre; ++i) {
         mbar_arrive_expect_tx(full_bar(i), L.stage_bytes);
-        tma_load_2d(sbase + uint32_t(i) * L.stage_bytes, &tmW, full_bar(i), (kb0 + i) * 128, n0);
+        load_w(sbase + uint32_t(i) * L.stage_bytes, full_bar(i), kb0 + i);
       }
       griddep_wait();
       griddep_launch_dependents();
       for (int i = 0; i < pre; ++i)
-        tma_load_2d(sbase + uint32_t(i) * L.stage_bytes + 16384u, &tmX, full_bar(i), (kb0 + i) * 128, 0);
+        tma_load_2d(sbase + uint32_t(i) * L.stage_bytes + 16384u, &tmX, full_bar(i), (kb0 + i) * kStageK, 0);
       int stage = pre % S;
       uint32_t phase = pre == S ? 1u : 0u;
       for (int i = pre; i < nkb + nr; ++i) {
@@ -262,11 +300,17 @@ __global__ void __launch_bounds__(kStreamThreads)
         const uint32_t st = sbase + uint32_t(stage) * L.stage_bytes, fb = full_bar(stage);
         mbar_arrive_expect_tx(fb, L.stage_bytes);
         if (i < nkb) {
-          tma_load_2d(st, &tmW, fb, (kb0 + i) * 128, n0);
-          tma_load_2d(st + 16384u, &tmX, fb, (kb0 + i) * 128, 0);
+          load_w(st, fb, kb0 + i);
+          tma_load_2d(st + 16384u, &tmX, fb, (kb0 + i) * kStageK, 0);
         } else {
-          tma_load_2d(st, &tmB, fb, (i - nkb) * 64, n0);
-          tma_load_2d(st + 16384u, &tmT, fb, (i - nkb) * 64, 0);
+          const int r0 = (i - nkb) * 64;
+          if constexpr (!MN) {
+            tma_load_2d(st, &tmV, fb, r0, n0);
+          } else {
+            tma_load_2d(st, &tmV, fb, n0, r0);
+            tma_load_2d(st + 8192u, &tmV, fb, n0 + 64, r0);
+          }
+          tma_load_2d(st + 16384u, &tmU, fb, r0, 0);
         }
         if (++stage == S) { stage = 0; phase ^= 1u; }
       }
@@ -274,8 +318,11 @@ __global__ void __launch_bounds__(kStreamThreads)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t id_rank = idesc_bf16(128, uint32_t(a.tok_pad), false, false);
+      const uint32_t id_bf16 = idesc_bf16(128, uint32_t(a.tok_pad), MN, false);
       const uint32_t sf_base = tmem + ncols - 16u * kStreamScaleBufs;
+      auto w_desc = [&](uint32_t st, uint32_t kk) {  // bf16: 16 values of K on
+        return MN ? smem_desc(st + kk * 2048u, 8192u, 1024u, SWZ_128B) : smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B);
+      };
       int stage = 0;
       uint32_t phase = 0, sf_tmem = 0;
       bool ok = true;
@@ -283,7 +330,13 @@ __global__ void __launch_bounds__(kStreamThreads)
         if (!wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL)) { ok = false; break; }
         tc_fence_after();
         const uint32_t st = sbase + uint32_t(stage) * L.stage_bytes, sx = st + 16384u;
-        if (i < nkb) {
+        if (i >= nkb) {
+          const uint32_t d = tmem + (DROP ? uint32_t(a.tok_pad) : 0u);
+          const int kk_n = imin(4, (a.r_pad - (i - nkb) * 64) / 16);
+          for (int kk = 0; kk < kk_n; ++kk)
+            umma_bf16(d, w_desc(st, uint32_t(kk)), smem_desc(sx + kk * 32u, 16u, 1024u, SWZ_128B), id_bf16,
+                      DROP ? (i - nkb | kk) != 0 : 1u);
+        } else if constexpr (FP8) {
           if ((i & 3) == 0) {
             const uint32_t n = uint32_t(i) >> 2, buf = n % kStreamScaleBufs;
             if (!wait_bounded(sffull0 + 8u * buf, (n / kStreamScaleBufs) & 1u, abort_flag, lim, SITE_TXMSG)) {
@@ -298,16 +351,18 @@ __global__ void __launch_bounds__(kStreamThreads)
               tmem_cp_scales(sf_tmem + 4u * c, smem_desc(src + 512u * c, 16u, 128u, SWZ_NONE));
             umma_commit(sfempty0 + 8u * buf);
           }
-          const uint32_t id = idesc_mxf8(128, uint32_t(a.tok_pad), false, false, uint32_t(i & 3));
+          const uint32_t id = idesc_mxf8(128, uint32_t(a.tok_pad), MN, false, uint32_t(i & 3));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_mxf8(tmem, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
+            umma_mxf8(tmem,
+                      MN ? smem_desc(st + kk * 4096u, 16384u, 1024u, SWZ_128B)
+                         : smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
                       smem_desc(sx + kk * 32u, 16u, 1024u, SWZ_128B), id, sf_tmem, sf_tmem + 4u, (i | kk) != 0);
         } else {
-          const int kk_n = imin(4, (a.r_pad - (i - nkb) * 64) / 16);
-          for (int kk = 0; kk < kk_n; ++kk)
-            umma_bf16(tmem, smem_desc(st + kk * 32u, 16u, 1024u, SWZ_128B),
-                      smem_desc(sx + kk * 32u, 16u, 1024u, SWZ_128B), id_rank, 1u);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem, w_desc(st, uint32_t(kk)), smem_desc(sx + kk * 32u, 16u, 1024u, SWZ_128B), id_bf16,
+                      (i | kk) != 0);
         }
         umma_commit(empty_bar(stage));
         if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -318,34 +373,36 @@ __global__ void __launch_bounds__(kStreamThreads)
     }
   } else {
     griddep_wait();
-    // Scale words: W's are one for the whole tile, the tokens' one each.  The
-    // four warps take the groups of four stages in turn, one buffer each.
-    const uint8_t* const ws = a.Ws + size_t(n0 >> 7) * size_t(nk);
-    const int last_group = (nk - 1) >> 2, x_blocks = (a.M + 127) / 128;
-    const uint32_t buf = uint32_t(warp - 2);
-    const uint32_t dst = sbase + L.off_sf + buf * kStreamScaleBytes + 16u * uint32_t(lane);
-    uint32_t use = 0;
-    for (int g = int(buf); g * 4 < nkb; g += kStreamScaleBufs) {
-      const int kb = kb0 + 4 * g;
-      uint32_t w = 0;
+    if constexpr (FP8) {
+      // Scale words: W's are one for the whole tile, the tokens' one each.  The
+      // four warps take the groups of four stages in turn, one buffer each.
+      const uint8_t* const ws = a.w_scales + size_t(n0 >> 7) * size_t(a.ws_row);
+      const int last_group = (nk - 1) >> 2, x_blocks = (a.M + 127) / 128;
+      const uint32_t buf = uint32_t(warp - 2);
+      const uint32_t dst = sbase + L.off_sf + buf * kStreamScaleBytes + 16u * uint32_t(lane);
+      uint32_t use = 0;
+      for (int g = int(buf); g * 4 < nkb; g += kStreamScaleBufs) {
+        const int kb = kb0 + 4 * g;
+        uint32_t w = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w |= uint32_t(ws[imin(kb + e, nk - 1)]) << (8 * e);
-      uint32_t x[8];
+        for (int e = 0; e < 4; ++e) w |= uint32_t(ws[size_t(imin(kb + e, nk - 1)) * size_t(a.ws_k)]) << (8 * e);
+        uint32_t x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (32 * i >= a.tok_pad) { x[i] = 0u; continue; }
-        const int tok = imin(32 * i + lane, a.M - 1);
-        const uint32_t lo = a.x_scales[scale_atom_offset(tok, kb & ~3, x_blocks) / 4];
-        const uint32_t hi = a.x_scales[scale_atom_offset(tok, imin((kb & ~3) + 4, 4 * last_group), x_blocks) / 4];
-        x[i] = __funnelshift_r(lo, hi, 8 * (kb & 3));
+        for (int i = 0; i < 8; ++i) {
+          if (32 * i >= a.tok_pad) { x[i] = 0u; continue; }
+          const int tok = imin(32 * i + lane, a.M - 1);
+          const uint32_t lo = a.x_scales[scale_atom_offset(tok, kb & ~3, x_blocks) / 4];
+          const uint32_t hi = a.x_scales[scale_atom_offset(tok, imin((kb & ~3) + 4, 4 * last_group), x_blocks) / 4];
+          x[i] = __funnelshift_r(lo, hi, 8 * (kb & 3));
+        }
+        if (!warp_wait_bounded(sfempty0 + 8u * buf, (use++ & 1u) ^ 1u, abort_flag, lim, SITE_VEMPTY)) break;
+        st_shared_v4(dst, make_uint4(w, w, w, w));
+        st_shared_v4(dst + 512u, make_uint4(x[0], x[1], x[2], x[3]));
+        st_shared_v4(dst + 1024u, make_uint4(x[4], x[5], x[6], x[7]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sffull0 + 8u * buf);
       }
-      if (!warp_wait_bounded(sfempty0 + 8u * buf, (use++ & 1u) ^ 1u, abort_flag, lim, SITE_VEMPTY)) break;
-      st_shared_v4(dst, make_uint4(w, w, w, w));
-      st_shared_v4(dst + 512u, make_uint4(x[0], x[1], x[2], x[3]));
-      st_shared_v4(dst + 1024u, make_uint4(x[4], x[5], x[6], x[7]));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sffull0 + 8u * buf);
     }
   }
 
@@ -360,6 +417,9 @@ __global__ void __launch_bounds__(kStreamThreads)
     if (have) {
       const int q = warp & 3;
       const uint32_t lane_base = uint32_t(q * 32) << 16;
+      const bool masked = DROP && split == 0;
+      DropState ds{};
+      if (masked) ds = drop_load(a.drop);
       for (int col = 0; col < a.tok_pad; col += 16) {
         uint32_t v[16];
         if (nkb > 0) {
@@ -368,6 +428,30 @@ __global__ void __launch_bounds__(kStreamThreads)
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = 0u;  // empty split: contributes zero
+        }
+        if (masked) {
+          // This lane's column i = n0 + 32 q + lane of dX is one of 8 that
+          // share a random block; each of the 8 lanes makes two of the 16
+          // tokens' blocks and hands the words around.
+          uint32_t u[16];
+          tmem_ld_x16(tmem + lane_base + uint32_t(a.tok_pad + col), u);
+          tmem_ld_wait();
+          const uint32_t c8 = uint32_t(n0 + q * 32 + lane) / 8u;
+          const int home = lane & 24, mine = lane & 7;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 r = drop_block(ds, c8, uint32_t(col + 8 * h + mine));
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              const uint32_t w0 = __shfl_sync(0xffffffffu, r.x, home + t), w1 = __shfl_sync(0xffffffffu, r.y, home + t);
+              const uint32_t w2 = __shfl_sync(0xffffffffu, r.z, home + t), w3 = __shfl_sync(0xffffffffu, r.w, home + t);
+              const uint32_t w = mine < 4 ? (mine < 2 ? w0 : w1) : (mine < 6 ? w2 : w3);
+              const bool keep = (mine & 1 ? w : w << 16) >= ds.thr_hi;
+              const int e = 8 * h + t;
+              const float x = __uint_as_float(u[e]) * a.drop.inv_keep;
+              v[e] = __float_as_uint(__uint_as_float(v[e]) + (keep ? x : 0.0f));
+            }
+          }
         }
         uint4* dst = reinterpret_cast<uint4*>(red + uint32_t(q * 32 + lane) * L.red_stride + col * 4);
 #pragma unroll
@@ -405,7 +489,7 @@ __global__ void __launch_bounds__(kStreamThreads)
       const float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (4 * t4 + e < a.M) a.Y[size_t(4 * t4 + e) * size_t(a.N) + size_t(n)] = __float2bfloat16_rn(v[e]);
+        if (4 * t4 + e < a.M) a.out[size_t(4 * t4 + e) * size_t(a.N) + size_t(n)] = __float2bfloat16_rn(v[e]);
     }
   }
   cluster_barrier_sync();  // peers keep their shared memory until every slice is done

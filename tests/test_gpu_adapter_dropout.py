@@ -62,6 +62,15 @@ SIZES = [  # M, d_in, d_out, r, p
     (128, 2048, 256, 40, 0.0),
     (4096, 256, 2048, 32, 0.1),
     (4096, 2048, 256, 32, 0.1),
+    # the kernels for few tokens: their limits, long contractions, every split
+    (128, 264, 1032, 16, 0.2),
+    (17, 4104, 136, 48, 0.3),
+    (40, 328, 6408, 128, 0.1),
+    (192, 6200, 6216, 8, 0.25),
+    (200, 6152, 6152, 32, 0.1),
+    (256, 6152, 264, 32, 0.5),
+    (512, 136, 264, 16, 0.5),
+    (513, 136, 264, 16, 0.5),
 ]
 
 

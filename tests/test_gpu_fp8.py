@@ -102,6 +102,15 @@ SIZES = [  # M, d_in, d_out, r, p
     (1000, 272, 1296, 64, 0.0),
     (4096, 256, 2048, 32, 0.1),
     (4096, 2048, 256, 32, 0.0),
+    # the kernels for few tokens: their limits, long contractions, every split
+    (128, 272, 1040, 16, 0.2),
+    (17, 4112, 144, 48, 0.3),
+    (40, 336, 6416, 128, 0.0),
+    (192, 6192, 6208, 8, 0.25),
+    (200, 6160, 6160, 32, 0.1),
+    (256, 6160, 272, 32, 0.0),
+    (64, 128, 128, 128, 0.5),
+    (65, 128, 128, 128, 0.5),
 ]
 
 
