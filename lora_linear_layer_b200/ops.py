@@ -216,11 +216,11 @@ def dequantize_weight(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor
     return W
 
 
-def _saved_bytes(M, r: int, fp8: bool):
-    """Bytes that the forward leaves for the backward: lora_bwd's workspace,
-    or with an 8-bit base the T at its start alone (the rest of that workspace
-    is scratch of M * max(d_in, d_out) bytes, not worth keeping)."""
-    return _workspace_bytes(M, r) // 2 if fp8 else _workspace_bytes(M, r)
+def _saved_bytes(M, r: int):
+    """Bytes that the forward leaves for the backward: T, at the start of
+    either workspace.  (The rest is scratch, with an 8-bit base of M *
+    max(d_in, d_out) bytes and more.)"""
+    return _workspace_bytes(M, r) // 2
 
 
 def _check_rng(p: float, rng: Optional[torch.Tensor]):
@@ -246,26 +246,25 @@ def lora_linear_adapter(X: torch.Tensor, W: torch.Tensor, W_scales: Optional[tor
     ab = (A.contiguous(), B.contiguous(), Y, scale)
     if fp8:
         lora_fwd_fp8(*args, W_scales.contiguous(), *ab, ws, p, rng)
-        return Y, ws[:max(_saved_bytes(M, r, True), 1)].clone()
-    lora_fwd_dropout(*args, *ab, p, rng, ws)
-    return Y, ws
+    else:
+        lora_fwd_dropout(*args, *ab, p, rng, ws)
+    return Y, ws[:max(_saved_bytes(M, r), 1)].clone()
 
 
 @lora_linear_adapter.register_fake
 def _lora_linear_adapter_fake(X, W, W_scales, A, B, scale, p, rng):
     M, d_in, d_out, r = _check(X, W, A, B)
     _check_rng(p, rng)
-    nbytes = _saved_bytes(M, r, W_scales is not None)
-    return X.new_empty((M, d_out)), X.new_empty((max(nbytes, 1),), dtype=torch.uint8)
+    return X.new_empty((M, d_out)), X.new_empty((max(_saved_bytes(M, r), 1),), dtype=torch.uint8)
 
 
-@torch.library.custom_op(f"{_LIB}::lora_linear_adapter_bwd", mutates_args=("saved",))
+@torch.library.custom_op(f"{_LIB}::lora_linear_adapter_bwd", mutates_args=())
 def lora_linear_adapter_bwd(X: torch.Tensor, W: torch.Tensor, W_scales: Optional[torch.Tensor], A: torch.Tensor,
                             B: torch.Tensor, dY: torch.Tensor, saved: torch.Tensor, scale: float, p: float,
                             rng: Optional[torch.Tensor],
                             fp32_grads: bool = False) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """(dX, dA, dB) of lora_linear_adapter for the same rng values; T is taken
-    from ``saved`` (over a bf16 base dT is written beside it)."""
+    """(dX, dA, dB) of lora_linear_adapter for the same rng values, with T from
+    ``saved``, which stays as it is (a graph may be gone through twice)."""
     M, d_in, d_out, r = _check(X, W, A, B)
     gdt = torch.float32 if fp32_grads else A.dtype
     dX = torch.empty((M, d_in), dtype=X.dtype, device=X.device)
@@ -274,12 +273,15 @@ def lora_linear_adapter_bwd(X: torch.Tensor, W: torch.Tensor, W_scales: Optional
     flags = LORA_BWD_T_SAVED | (LORA_BWD_FP32_GRADS if fp32_grads else 0)
     args = (X.contiguous(), W.contiguous())
     rest = (A.contiguous(), B.contiguous(), dY.contiguous(), dX, dA, dB, scale)
-    if W_scales is not None:
-        ws = torch.empty(max(lora_fp8_workspace_size(M, d_in, d_out, r), 1), dtype=torch.uint8, device=X.device)
-        ws[:saved.numel()].copy_(saved)
+    fp8 = W_scales is not None
+    nbytes = lora_fp8_workspace_size(M, d_in, d_out, r) if fp8 else _workspace_bytes(M, r)
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=X.device)
+    t_bytes = _saved_bytes(M, r)
+    ws[:t_bytes].copy_(saved[:t_bytes])
+    if fp8:
         lora_bwd_fp8(*args, W_scales.contiguous(), *rest, ws, p, rng, flags)
     else:
-        lora_bwd_dropout(*args, *rest, p, rng, saved, flags)
+        lora_bwd_dropout(*args, *rest, p, rng, ws, flags)
     return dX, dA, dB
 
 

@@ -267,3 +267,58 @@ def test_tensors_of_a_call_share_a_device(gpu):
         gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y.t(), 1.0, 0.1, rng_tensor(0, 0), ws)
     with pytest.raises(gpu.LoraError):
         gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, 1.0, 0.1, rng_tensor(0, 0), ws[:256])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_module_on_an_empty_batch(gpu, fp8):
+    m = layer(64, 48, 8, 0.1, fp8)
+    x = torch.empty(2, 0, 64, dtype=BF16, device="cuda", requires_grad=True)
+    y = m(x)
+    assert y.shape == (2, 0, 48)
+    y.sum().backward()
+    assert x.grad.shape == x.shape and (m.lora_A.grad == 0).all() and (m.lora_B.grad == 0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_backward_twice_through_one_graph(gpu, fp8):
+    m = layer(256, 136 if not fp8 else 144, 8, 0.2, fp8)
+    x = make(77, 256, m.d_out, 8)["X"].cuda().requires_grad_(True)
+    y = m(x)
+    dy = torch.ones_like(y)
+    first = torch.autograd.grad(y, (x, m.lora_A, m.lora_B), dy, retain_graph=True)
+    for a, b in zip(first, torch.autograd.grad(y, (x, m.lora_A, m.lora_B), dy)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_offsets_past_32_bits(gpu, fp8):
+    """X of 2.4 * 10^9 elements: rows on both sides of 2^31 elements, and the
+    last, against the reference."""
+    from lora_linear_layer_b200 import ops
+    M, K, N, r, p = 590001, 4096, 64, 8, 0.25
+    t = make(8, K, N, r)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    X = torch.empty(M, K, dtype=BF16, device="cuda")
+    for i in range(0, M, 65536):
+        X[i:i + 65536] = torch.randn(min(65536, M - i), K, generator=g, device="cuda").to(BF16)
+    W, A, B = (t[k].cuda() for k in ("W", "A", "B"))
+    Wq, Ws = ops.quantize_weight(W) if fp8 else (W, None)
+    rng = rng_tensor(7, 8)
+    Y, saved = torch.ops.lora_b200.lora_linear_adapter(X, Wq, Ws, A, B, 1.0, p, rng)
+    dY = torch.ones(M, N, dtype=BF16, device="cuda")
+    dX, _, _ = torch.ops.lora_b200.lora_linear_adapter_bwd(X, Wq, Ws, A, B, dY, saved, 1.0, p, rng)
+    assert gpu.lora_get_device_status() == 0
+    edge = 2 ** 31 // K
+    rows = torch.tensor([0, 127, edge - 1, edge, edge + 1, M - 130, M - 1])
+    keep = np.concatenate([R.keep_mask(7, 8, 1, K, p) if i == 0 else _mask_row(7, 8, int(i), K, p) for i in rows])
+    Wv = values(Wq, Ws) if fp8 else R.f64(W)
+    ref = R.layer(R.f64(X[rows.cuda()]), Wv, R.f64(A), R.f64(B), 1.0, dY=np.ones((len(rows), N)), mask=keep, p=p,
+                  fp8=fp8)
+    R.check("Y", host(Y[rows.cuda()]), ref["Y"])
+    R.check("dX", host(dX[rows.cuda()]), ref["dX"])
+
+
+def _mask_row(seed, offset, i, K, p):
+    words = R.philox(np.arange(K // 8), np.full(K // 8, i), np.full(K // 8, offset), np.zeros(K // 8, dtype=int), seed, 0)
+    lanes = np.stack([h for w in words for h in (w & np.uint64(0xFFFF), w >> np.uint64(16))], axis=-1)
+    return (lanes.reshape(1, K) >= R.threshold(p))

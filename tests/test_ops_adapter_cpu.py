@@ -23,7 +23,7 @@ def test_fake_shapes(fp8):
         rng = torch.empty(2, dtype=torch.int64, device="cuda")
         Y, saved = torch.ops.lora_b200.lora_linear_adapter(X, W, Ws, A, B, 2.0, 0.1, rng)
         assert Y.shape == (32, 48) and Y.dtype == BF16 and saved.dtype == torch.uint8
-        assert saved.numel() == (1 if fp8 else 2) * 32 * 16 * 2
+        assert saved.numel() == 32 * 16 * 2
         for f32 in (False, True):
             dX, dA, dB = torch.ops.lora_b200.lora_linear_adapter_bwd(X, W, Ws, A, B, Y, saved, 2.0, 0.1, rng, f32)
             assert dX.shape == X.shape and dA.shape == A.shape and dB.shape == B.shape
@@ -68,6 +68,5 @@ def test_module_traces_without_a_graph_break(train):
 
 def test_saved_bytes_are_the_librarys(built_lib):
     for M, r in ((1, 8), (5, 16), (300, 24), (4096, 128)):
-        assert ops._saved_bytes(M, r, False) == built_lib.lora_bwd_workspace_size(M, 64, 64, r)
-        assert 2 * ops._saved_bytes(M, r, True) == built_lib.lora_bwd_workspace_size(M, 64, 64, r)
-        assert built_lib.lora_fp8_workspace_size(M, 64, 64, r) >= ops._saved_bytes(M, r, True)
+        assert 2 * ops._saved_bytes(M, r) == built_lib.lora_bwd_workspace_size(M, 64, 64, r)
+        assert built_lib.lora_fp8_workspace_size(M, 64, 64, r) >= ops._saved_bytes(M, r)
