@@ -467,8 +467,8 @@ def lora_restore(W_src, W_dst, stream=None) -> None:
 
 # ------------------------------------- dropout and the 8-bit base ----
 
-def _bad(t, name: str, dtype, shape: Tuple[int, ...], device):
-    """Raises what is wrong with an argument that _ok refused."""
+def _bad(t, name: str, dtype, shape: Tuple[int, ...], index: int):
+    """Raises what is wrong with an argument that _pointers refused."""
     torch = _tm()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -480,19 +480,22 @@ def _bad(t, name: str, dtype, shape: Tuple[int, ...], device):
         raise ValueError(f"{name} must be contiguous")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _arg(t, name: str, dtype, shape: Tuple[int, ...], index: int):
-    """The pointer of a contiguous tensor of this type and shape on CUDA
-    device ``index``.  (One expression for the usual case: a call checks ten
-    tensors, which is host time of the order of a small layer's kernels.)"""
-    try:
-        if t.dtype is dtype and t.get_device() == index and index >= 0 and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _bad(t, name, dtype, shape, f"cuda:{index}")
+def _pointers(tensors, index: int) -> list:
+    """The pointers of contiguous tensors, given as (tensor, name, dtype,
+    shape), on CUDA device ``index``.  (One expression a tensor in the usual
+    case: a call checks up to ten, and at a few tokens the host's time is the
+    layer's.)"""
+    out = []
+    for t, name, dtype, shape in tensors:
+        if (getattr(t, "dtype", None) is dtype and t.get_device() == index >= 0 and t.shape == shape
+                and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
+            _bad(t, name, dtype, shape, index)
+    return out
 
 
 def _workspace_arg(workspace, index: int):
@@ -533,19 +536,21 @@ def _layer(name, X, W, Ws, A, B, outs, scale, p, rng, workspace, flags, stream):
         raise ValueError(f"X and B must be 2-D, got {X.dim()}-D and {B.dim()}-D")
     M, d_in = X.shape
     d_out, r = B.shape
-    i = X.get_device()
-    args = [_arg(X, "X", bf16, (M, d_in), i)]
+    shapes = {"dX": (M, d_in), "dA": (r, d_in), "dB": (d_out, r)}
+    tensors = [(X, "X", bf16, (M, d_in))]
     if Ws is None:
-        args.append(_arg(W, "W", bf16, (d_out, d_in), i))
+        tensors.append((W, "W", bf16, (d_out, d_in)))
     else:
-        args.append(_arg(W, "Wq", torch.float8_e4m3fn, (d_out, d_in), i))
-        args.append(_arg(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), i))
-    args.append(_arg(A, "A", bf16, (r, d_in), i))
-    args.append(_arg(B, "B", bf16, (d_out, r), i))
+        tensors.append((W, "Wq", torch.float8_e4m3fn, (d_out, d_in)))
+        tensors.append((Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in)))
+    tensors.append((A, "A", bf16, (r, d_in)))
+    tensors.append((B, "B", bf16, (d_out, r)))
     for n, t, dtype in outs:
-        shape = (r, d_in) if n == "dA" else (d_out, r) if n == "dB" else (M, d_in) if n == "dX" else (M, d_out)
-        args.append(_arg(t, n, dtype, shape, i))
-    args += (M, d_in, d_out, r, scale, p, None if rng is None else _arg(rng, "rng", torch.int64, (2,), i))
+        tensors.append((t, n, dtype, shapes.get(n, (M, d_out))))
+    i = X.get_device()
+    args = _pointers(tensors, i)
+    args += (M, d_in, d_out, r, scale, p,
+             None if rng is None else _pointers(((rng, "rng", torch.int64, (2,)),), i)[0])
     args += _workspace_arg(workspace, i)
     if flags is not None:
         args.append(flags)
@@ -597,8 +602,8 @@ def _quant(name, W, Wq, Ws, order, stream):
         raise ValueError("W must be a 2-D tensor")
     d_out, d_in = W.shape
     i = W.get_device()
-    p = (_arg(W, "W", torch.bfloat16, (d_out, d_in), i), _arg(Wq, "Wq", torch.float8_e4m3fn, (d_out, d_in), i),
-         _arg(Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in), i))
+    p = _pointers(((W, "W", torch.bfloat16, (d_out, d_in)), (Wq, "Wq", torch.float8_e4m3fn, (d_out, d_in)),
+                   (Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in))), i)
     _call(name, i, (p[order[0]], p[order[1]], p[order[2]], d_out, d_in), stream)
 
 
