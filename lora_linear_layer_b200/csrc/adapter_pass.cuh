@@ -234,27 +234,27 @@ __global__ void __launch_bounds__(pass_threads(RCW, P_MN), pass_workers(RCW, P_M
     // can, and pointers run along.
     constexpr int kRows = 128 / kPassWorkers;
     if constexpr (!P_MN) {
-      // Eight rows at a time, 4 lanes a row, 32 consecutive values a lane: four
-      // 16-byte chunks of sub-stage c / 2.  The lanes of the second sub-stage
-      // take theirs in the order 2, 3, 0, 1: then the 8 lanes of two rows touch
-      // 8 different bank groups (the swizzle gives the other two bits).
+      // Eight rows at a time, 4 lanes a row; a lane has 16 consecutive values
+      // (two 16-byte chunks) of each sub-stage, so that the row's codes leave
+      // in two stores of 64 consecutive bytes.  The 8 lanes of two rows touch
+      // 8 different bank groups: even chunks of one row, odd ones of the other.
       constexpr int kIts = kRows / 8;
       const int c = lane & 3, r8 = lane >> 2;
       const int row0 = i0 + w * kRows + r8;
-      const uint32_t flip = uint32_t(c >> 1) * 2u;
-      const uint32_t row_at = uint32_t(c >> 1) * L.sub_bytes + uint32_t(w * kRows + r8) * 128u;
-      uint32_t at[4];  // inside a stage, of a lane's chunks 0 ^ flip, 1 ^ flip, ...
+      uint32_t at[4];  // inside a stage: chunks 2 c and 2 c + 1 of the first sub-stage, then of the second
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) at[j] = row_at + ((uint32_t(c & 1) * 4u + (j ^ flip)) ^ uint32_t(r8)) * 16u;
+      for (uint32_t j = 0; j < 4; ++j)
+        at[j] = (j >> 1) * L.sub_bytes + uint32_t(w * kRows + r8) * 128u +
+                ((uint32_t(c) * 2u + (j & 1u)) ^ uint32_t(r8)) * 16u;
       const bool any = i0 + w * kRows < a.rows;  // (rows past the end are zero fill)
-      uint8_t* code = QUANT ? a.codes + size_t(row0) * size_t(a.K) + size_t(kb0) * 128 + size_t(c * 32) : nullptr;
+      uint8_t* code = QUANT ? a.codes + size_t(row0) * size_t(a.K) + size_t(kb0) * 128 + size_t(c * 16) : nullptr;
       const size_t code_step = size_t(8) * size_t(a.K);
       const int row_blocks = (a.rows + 127) / 128;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait_bounded(full_bar(stage), phase, abort_flag, lim, SITE_FULL)) break;
         if (any) {
           const uint32_t st = sbase + uint32_t(stage) * L.stage_bytes;
-          const int k = kb * 128 + c * 32;
+          const int k = kb * 128 + c * 16;
           uint4 v[kIts][4];
 #pragma unroll
           for (int it = 0; it < kIts; ++it)
@@ -278,9 +278,8 @@ __global__ void __launch_bounds__(pass_threads(RCW, P_MN), pass_workers(RCW, P_M
               if (row0 + 8 * it < a.rows) {
                 uint8_t* const dst = code + size_t(it) * code_step;
                 // (K is a multiple of 16)
-                if (k + int(flip) * 8 < a.K) *reinterpret_cast<uint4*>(dst + flip * 8u) = make_uint4(q0.x, q0.y, q1.x, q1.y);
-                if (k + 16 - int(flip) * 8 < a.K)
-                  *reinterpret_cast<uint4*>(dst + 16u - flip * 8u) = make_uint4(q2.x, q2.y, q3.x, q3.y);
+                if (k < a.K) *reinterpret_cast<uint4*>(dst) = make_uint4(q0.x, q0.y, q1.x, q1.y);
+                if (k + 64 < a.K) *reinterpret_cast<uint4*>(dst + 64) = make_uint4(q2.x, q2.y, q3.x, q3.y);
                 if (c == 0) scale[it * 128] = uint8_t(b);
               }
             }
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(pass_threads(RCW, P_MN), pass_workers(RCW, P_M
 #pragma unroll
               for (uint32_t j = 0; j < 4; ++j)
                 st_shared_v4(st + at[j] + uint32_t(it) * 1024u,
-                             drop_bf16x8(v[it][j], drop_block(ds, c8 + (j ^ flip), uint32_t(row0 + 8 * it)), ds.thr_hi));
+                             drop_bf16x8(v[it][j], drop_block(ds, c8 + (j >> 1) * 8u + (j & 1u), uint32_t(row0 + 8 * it)), ds.thr_hi));
           }
         }
         if (drop) fence_proxy_async_smem();

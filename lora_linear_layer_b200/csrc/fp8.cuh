@@ -195,39 +195,35 @@ __global__ void __launch_bounds__(kQuantThreads)
 }
 
 // Wq, Ws -> W (bf16): each value q 2^(b - 127) rounded once (it is exact
-// unless it is below bf16's normal range).
+// unless it is below bf16's normal range).  Eight values a lane, so that a
+// warp's store is 512 consecutive bytes of two rows (16 values a lane, stored
+// in two halves of each 32-byte sector, took 38 us instead of 23 on 14336 x
+// 4096).
 __global__ void __launch_bounds__(kQuantThreads)
     dequantize_block_kernel(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Ws, uint8_t* __restrict__ W,
                             int32_t rows, int32_t cols, int32_t col_blocks) {
   griddep_wait();
   griddep_launch_dependents();
   const int cb = int(blockIdx.x) % col_blocks, rb = int(blockIdx.x) / col_blocks;
-  const int col = cb * kQBlock + int(threadIdx.x & 7u) * 16;
-  const int row0 = rb * kQBlock + int(threadIdx.x >> 3);
+  const int col = cb * kQBlock + int(threadIdx.x & 15u) * 8;
+  const int row0 = rb * kQBlock + int(threadIdx.x >> 4);
   if (col >= cols) return;
-  uint4 q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = row0 + 32 * i;
-    q[i] = row < rows ? __ldcs(reinterpret_cast<const uint4*>(Wq + size_t(row) * size_t(cols) + size_t(col)))
-                      : make_uint4(0, 0, 0, 0);
-  }
   const float s = e8m0_value(Ws[blockIdx.x]);
+  uint2 q[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = row0 + 32 * i;
+  for (int i = 0; i < 8; ++i) {
+    const int row = imin(row0 + 16 * i, rows - 1);
+    q[i] = __ldcs(reinterpret_cast<const uint2*>(Wq + size_t(row) * size_t(cols) + size_t(col)));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 16 * i;
     if (row >= rows) return;
-    uint32_t o[8];
-    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 lo = e4m3x2_to_f32(w[j]), hi = e4m3x2_to_f32(w[j] >> 16);
-      o[2 * j] = pack_bf16x2(lo.x * s, lo.y * s);
-      o[2 * j + 1] = pack_bf16x2(hi.x * s, hi.y * s);
-    }
-    uint4* dst = reinterpret_cast<uint4*>(W + (size_t(row) * size_t(cols) + size_t(col)) * 2);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    const float2 a = e4m3x2_to_f32(q[i].x), b = e4m3x2_to_f32(q[i].x >> 16);
+    const float2 c = e4m3x2_to_f32(q[i].y), d = e4m3x2_to_f32(q[i].y >> 16);
+    *reinterpret_cast<uint4*>(W + (size_t(row) * size_t(cols) + size_t(col)) * 2) =
+        make_uint4(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s), pack_bf16x2(c.x * s, c.y * s),
+                   pack_bf16x2(d.x * s, d.y * s));
   }
 }
 
