@@ -68,19 +68,23 @@ struct PassCfg {
   PassArgs args;
 };
 
-// Three stages (36 KB each for K-major P at r = 16: two blocks per SM); the
-// splits of a row tile form one cluster, as many as fill the resident block
-// slots, at most 8 and at least 256 values of the contraction each.
-void pick_pass(int64_t rows, int64_t K, int r, bool p_mn, bool r_mn, int out_mode, int64_t launch_tiles, int sm_count,
-               PassCfg& c) {
+// Three stages where two blocks share an SM (37 KB each at r = 16), else as
+// many as fit, at most six; the splits of a row tile form one cluster, as many
+// as fill the resident block slots, at most 8 and at least 256 values of the
+// contraction each.
+void pick_pass(int64_t rows, int64_t K, int r, bool p_mn, bool r_mn, bool quant, int out_mode, int64_t launch_tiles,
+               int sm_count, PassCfg& c) {
   const int r_pad = r_pad_of(r);
   c.RCW = rcw_of(r_pad);
   PassArgs& a = c.args;
   std::memset(&a, 0, sizeof(a));
   a.n_rchunks = (r_pad + c.RCW - 1) / c.RCW;
-  a.stages = 3;
-  c.smem = PassLayout(p_mn, r_mn, c.RCW, r_pad, a.n_rchunks, a.stages).total + 1024;
-  const int per_sm = std::max(1, std::min<int>(int(kSmemPerSM / (c.smem + 1024)), 2048 / pass_threads(c.RCW, p_mn)));
+  auto smem = [&](int stages) { return PassLayout(p_mn, r_mn, c.RCW, r_pad, a.n_rchunks, stages).total + 1024; };
+  a.stages = pass_workers(c.RCW, p_mn, quant) == 16 ? 6 : 3;
+  while (a.stages > 2 && smem(a.stages) > kSmemMax) --a.stages;
+  c.smem = smem(a.stages);
+  const int per_sm =
+      std::max(1, std::min<int>(int(kSmemPerSM / (c.smem + 1024)), 2048 / pass_threads(c.RCW, p_mn, quant)));
   const int block_k = p_mn ? 64 : 128;
   const int nb = int((K + block_k - 1) / block_k);
   const int tiles = int(std::max<int64_t>(1, launch_tiles));
@@ -127,7 +131,7 @@ lora_status_t launch_pass_t(const PassMaps& m0, const PassCfg& c0, const PassMap
   const dim3 cl(1, unsigned(c0.args.splits), 1);
   const PassMaps& second = m1 != nullptr ? *m1 : m0;
   const int ta = atoms.bytes != nullptr ? kAtomBlocks : 0;
-  return launch_ex("adapter pass", kern, dim3(unsigned(t0 + t1 + ta), unsigned(c0.args.splits)), dim3(pass_threads(RCW, P_MN)),
+  return launch_ex("adapter pass", kern, dim3(unsigned(t0 + t1 + ta), unsigned(c0.args.splits)), dim3(pass_threads(RCW, P_MN, QUANT)),
                    smem, st, &cl, m0.p, m0.r, second.p, second.r, c0.args, c1 != nullptr ? c1->args : c0.args,
                    int32_t(t0), int32_t(t0 + t1), atoms);
 }
@@ -151,7 +155,7 @@ struct Rounded {
 lora_status_t launch_down(const void* X, const void* A, int64_t M, int64_t d_in, int32_t r, float scale,
                           const DropArgs& drop, __nv_bfloat16* Tws, const Rounded* q, int sm_count, cudaStream_t st) {
   PassCfg c;
-  pick_pass(M, d_in, r, false, false, OUT_ROWS_RPAD, (M + 127) / 128, sm_count, c);
+  pick_pass(M, d_in, r, false, false, q != nullptr, OUT_ROWS_RPAD, (M + 127) / 128, sm_count, c);
   c.args.out = Tws;
   c.args.scale = scale * drop.inv_keep;
   c.args.drop = drop;
@@ -499,7 +503,7 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
   }
   {
     PassCfg p;
-    pick_pass(M, d_out, r, false, true, OUT_ROWS_RPAD, (M + 127) / 128, sms, p);
+    pick_pass(M, d_out, r, false, true, fp8, OUT_ROWS_RPAD, (M + 127) / 128, sms, p);
     p.args.out = at.dT;
     p.args.scale = scale;
     PassMaps m;
@@ -521,8 +525,8 @@ lora_status_t adapter_bwd_run(const void* X, const Base& W, const void* A, const
     // 215 us with dB's first, and 187 us as two launches).
     PassCfg cb, ca;
     const int64_t tiles = (d_out + 127) / 128 + (d_in + 127) / 128;
-    pick_pass(d_in, M, r, true, true, OUT_COLS_R, tiles, sms, ca);
-    pick_pass(d_out, M, r, true, true, OUT_ROWS_R, tiles, sms, cb);
+    pick_pass(d_in, M, r, true, true, false, OUT_COLS_R, tiles, sms, ca);
+    pick_pass(d_out, M, r, true, true, false, OUT_ROWS_R, tiles, sms, cb);
     resplit_pass(cb, ca.args.splits, true);
     cb.args.out = reinterpret_cast<__nv_bfloat16*>(dB);
     cb.args.out_f32 = f32 ? 1 : 0;

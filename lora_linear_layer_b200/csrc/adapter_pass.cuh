@@ -29,11 +29,17 @@
 
 namespace lora {
 
-// Warps that work on the stages, beside the TMA and the MMA warp: 8, and two
-// blocks an SM, while the rank's operand is narrow; above r = 32 K-major
-// stages are 48 KB and more, one block fits an SM, and it gets 16.
-__host__ __device__ constexpr int pass_workers(int rcw, bool p_mn) { return rcw == 64 && !p_mn ? 16 : 8; }
-__host__ __device__ constexpr int pass_threads(int rcw, bool p_mn) { return 64 + 32 * pass_workers(rcw, p_mn); }
+// Warps that work on the stages, beside the TMA and the MMA warp: 16, one
+// block an SM and a deep ring, where P is rounded (X[8192, 4096] at r = 16: 21
+// us against 24 us with two blocks of 8) or the rank's operand is wide (stages
+// of 48 KB and more); else 8 and two blocks an SM (masked, X[32768, 4096]: 78
+// us against 83 us).
+__host__ __device__ constexpr int pass_workers(int rcw, bool p_mn, bool quant) {
+  return !p_mn && (quant || rcw == 64) ? 16 : 8;
+}
+__host__ __device__ constexpr int pass_threads(int rcw, bool p_mn, bool quant) {
+  return 64 + 32 * pass_workers(rcw, p_mn, quant);
+}
 
 struct PassArgs {
   int32_t rows;           // output rows (size of the i dimension)
@@ -71,13 +77,13 @@ struct PassLayout {
 };
 
 template <bool P_MN, int RCW, bool QUANT>
-__global__ void __launch_bounds__(pass_threads(RCW, P_MN), pass_workers(RCW, P_MN) == 16 ? 1 : 2)
+__global__ void __launch_bounds__(pass_threads(RCW, P_MN, QUANT), pass_workers(RCW, P_MN, QUANT) == 16 ? 1 : 2)
     adapter_pass_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmR0,
                         const __grid_constant__ CUtensorMap tmP1, const __grid_constant__ CUtensorMap tmR1,
                         const __grid_constant__ PassArgs a0, const __grid_constant__ PassArgs a1,
                         const int32_t x_split, const int32_t x_atoms, const __grid_constant__ ScaleAtomArgs atoms) {
   static_assert(!(P_MN && QUANT), "codes are written row by row");
-  constexpr int kPassWorkers = pass_workers(RCW, P_MN), kPassThreads = pass_threads(RCW, P_MN);
+  constexpr int kPassWorkers = pass_workers(RCW, P_MN, QUANT), kPassThreads = pass_threads(RCW, P_MN, QUANT);
   if constexpr (QUANT) {
     if (int(blockIdx.x) >= x_atoms) {  // blocks behind the row tiles: the other operand's scales
       griddep_wait();
