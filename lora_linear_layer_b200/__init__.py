@@ -507,16 +507,19 @@ def _workspace_arg(workspace, index: int):
     return workspace.data_ptr(), workspace.nbytes
 
 
-def _scales_shape(d_out: int, d_in: int) -> Tuple[int, int]:
-    return (d_out + 127) // 128, (d_in + 127) // 128
+_current_device = None
 
 
 def _call(name, index: int, args, stream):
     """Calls the library's function `name` with `args` and the stream, with
     the tensors' device current (the library launches on the current one)."""
+    global _current_device
     torch = _tm()
-    fn = getattr(lib(), name)
-    if index == torch._C._cuda_getDevice():
+    if _current_device is None:
+        # without the lazy-initialisation check (the tensors are on a device)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    fn = getattr(_lib_handle or lib(), name)
+    if index == _current_device():
         code = fn(*args, _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream))
     else:
         with torch.cuda.device(index):
@@ -525,58 +528,65 @@ def _call(name, index: int, args, stream):
         raise LoraError(code, name)
 
 
-def _layer(name, X, W, Ws, A, B, outs, scale, p, rng, workspace, flags, stream):
-    """A layer call: checks the tensors, all on X's device; `outs` are the
-    tensors after B, as (name, tensor, dtype)."""
+def _sizes(X, B):
     torch = _tm()
-    bf16 = torch.bfloat16
     if not isinstance(X, torch.Tensor) or not isinstance(B, torch.Tensor):
         raise TypeError("X and B must be torch.Tensors")
     if X.dim() != 2 or B.dim() != 2:
         raise ValueError(f"X and B must be 2-D, got {X.dim()}-D and {B.dim()}-D")
-    M, d_in = X.shape
-    d_out, r = B.shape
-    shapes = {"dX": (M, d_in), "dA": (r, d_in), "dB": (d_out, r)}
-    tensors = [(X, "X", bf16, (M, d_in))]
-    if Ws is None:
-        tensors.append((W, "W", bf16, (d_out, d_in)))
-    else:
-        tensors.append((W, "Wq", torch.float8_e4m3fn, (d_out, d_in)))
-        tensors.append((Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in)))
-    tensors.append((A, "A", bf16, (r, d_in)))
-    tensors.append((B, "B", bf16, (d_out, r)))
-    for n, t, dtype in outs:
-        tensors.append((t, n, dtype, shapes.get(n, (M, d_out))))
+    return (*X.shape, *B.shape)
+
+
+def _base(base, d_out: int, d_in: int):
+    """The checks of a base weight: (W,) or (Wq, Ws)."""
+    torch = _tm()
+    if len(base) == 1:
+        return ((base[0], "W", torch.bfloat16, (d_out, d_in)),)
+    return ((base[0], "Wq", torch.float8_e4m3fn, (d_out, d_in)),
+            (base[1], "Ws", torch.float8_e8m0fnu, ((d_out + 127) // 128, (d_in + 127) // 128)))
+
+
+def _rng_arg(rng, index: int):
+    return None if rng is None else _pointers(((rng, "rng", _torch.int64, (2,)),), index)[0]
+
+
+def _layer_fwd(name, X, base, A, B, Y, scale, p, rng, workspace, stream):
+    """A forward: checks the tensors, all on X's device, and calls `name`."""
+    M, d_in, d_out, r = _sizes(X, B)
+    bf16 = _torch.bfloat16
     i = X.get_device()
-    args = _pointers(tensors, i)
-    args += (M, d_in, d_out, r, scale, p,
-             None if rng is None else _pointers(((rng, "rng", torch.int64, (2,)),), i)[0])
-    args += _workspace_arg(workspace, i)
-    if flags is not None:
-        args.append(flags)
+    args = _pointers(((X, "X", bf16, (M, d_in)), *_base(base, d_out, d_in), (A, "A", bf16, (r, d_in)),
+                      (B, "B", bf16, (d_out, r)), (Y, "Y", bf16, (M, d_out))), i)
+    args += (M, d_in, d_out, r, scale, p, _rng_arg(rng, i), *_workspace_arg(workspace, i))
     _call(name, i, args, stream)
 
 
-def _layer_bwd(name, X, W, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream):
-    torch = _tm()
-    bf16 = torch.bfloat16
-    gdt = torch.float32 if int(flags) & LORA_BWD_FP32_GRADS else bf16
-    _layer(name, X, W, Ws, A, B, (("dY", dY, bf16), ("dX", dX, bf16), ("dA", dA, gdt), ("dB", dB, gdt)), scale, p, rng,
-           workspace, int(flags), stream)
+def _layer_bwd(name, X, base, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream):
+    """A backward, likewise."""
+    M, d_in, d_out, r = _sizes(X, B)
+    bf16 = _torch.bfloat16
+    flags = int(flags)
+    gdt = _torch.float32 if flags & LORA_BWD_FP32_GRADS else bf16
+    i = X.get_device()
+    args = _pointers(((X, "X", bf16, (M, d_in)), *_base(base, d_out, d_in), (A, "A", bf16, (r, d_in)),
+                      (B, "B", bf16, (d_out, r)), (dY, "dY", bf16, (M, d_out)), (dX, "dX", bf16, (M, d_in)),
+                      (dA, "dA", gdt, (r, d_in)), (dB, "dB", gdt, (d_out, r))), i)
+    args += (M, d_in, d_out, r, scale, p, _rng_arg(rng, i), *_workspace_arg(workspace, i), flags)
+    _call(name, i, args, stream)
 
 
 def lora_fwd_dropout(X, W, A, B, Y, scale: float, p: float, rng, workspace, stream=None) -> None:
     """Y = X W^T + T B^T with T = scale/(1-p) (m * X) A^T, the mask m drawn
     from ``rng``, an int64 CUDA tensor [seed, offset] (see include/lora.h).
     ``workspace`` (lora_bwd_workspace_size bytes) receives T."""
-    _layer("lora_fwd_dropout", X, W, None, A, B, (("Y", Y, _tm().bfloat16),), scale, p, rng, workspace, None, stream)
+    _layer_fwd("lora_fwd_dropout", X, (W,), A, B, Y, scale, p, rng, workspace, stream)
 
 
 def lora_bwd_dropout(X, W, A, B, dY, dX, dA, dB, scale: float, p: float, rng, workspace, flags: int = 0,
                      stream=None) -> None:
     """The backward of lora_fwd_dropout for the same ``rng`` values; with
     LORA_BWD_T_SAVED the workspace is the one the forward left T in."""
-    _layer_bwd("lora_bwd_dropout", X, W, None, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
+    _layer_bwd("lora_bwd_dropout", X, (W,), A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
 
 
 def lora_fp8_workspace_size(M: int, d_in: int, d_out: int, r: int) -> int:
@@ -587,13 +597,13 @@ def lora_fwd_fp8(X, Wq, Ws, A, B, Y, scale: float, workspace, p: float = 0.0, rn
     """Y = Xq Wq^T + T B^T over an 8-bit base: Wq float8_e4m3fn [d_out, d_in],
     Ws float8_e8m0fnu [ceil(d_out/128), ceil(d_in/128)] (see include/lora.h);
     ``workspace`` of lora_fp8_workspace_size bytes."""
-    _layer("lora_fwd_fp8", X, Wq, Ws, A, B, (("Y", Y, _tm().bfloat16),), scale, p, rng, workspace, None, stream)
+    _layer_fwd("lora_fwd_fp8", X, (Wq, Ws), A, B, Y, scale, p, rng, workspace, stream)
 
 
 def lora_bwd_fp8(X, Wq, Ws, A, B, dY, dX, dA, dB, scale: float, workspace, p: float = 0.0, rng=None, flags: int = 0,
                  stream=None) -> None:
     """The backward of lora_fwd_fp8: dX through Wq, dA and dB of the adapter."""
-    _layer_bwd("lora_bwd_fp8", X, Wq, Ws, A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
+    _layer_bwd("lora_bwd_fp8", X, (Wq, Ws), A, B, dY, dX, dA, dB, scale, p, rng, workspace, flags, stream)
 
 
 def _quant(name, W, Wq, Ws, order, stream):
@@ -602,8 +612,7 @@ def _quant(name, W, Wq, Ws, order, stream):
         raise ValueError("W must be a 2-D tensor")
     d_out, d_in = W.shape
     i = W.get_device()
-    p = _pointers(((W, "W", torch.bfloat16, (d_out, d_in)), (Wq, "Wq", torch.float8_e4m3fn, (d_out, d_in)),
-                   (Ws, "Ws", torch.float8_e8m0fnu, _scales_shape(d_out, d_in))), i)
+    p = _pointers(((W, "W", torch.bfloat16, (d_out, d_in)), *_base((Wq, Ws), d_out, d_in)), i)
     _call(name, i, (p[order[0]], p[order[1]], p[order[2]], d_out, d_in), stream)
 
 

@@ -269,6 +269,24 @@ def test_tensors_of_a_call_share_a_device(gpu):
         gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, 1.0, 0.1, rng_tensor(0, 0), ws[:256])
 
 
+def test_missing_tensors_are_named(gpu):
+    t = {k: v.cuda() for k, v in make(8, 64, 64, 8).items()}
+    Y = torch.empty(8, 64, dtype=BF16, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    codes = t["W"].to(torch.float8_e4m3fn)
+    for missing in (None, 3):
+        with pytest.raises(TypeError, match="Ws"):
+            gpu.lora_fwd_fp8(t["X"], codes, missing, t["A"], t["B"], Y, 1.0, ws)
+        with pytest.raises(TypeError, match="Wq"):
+            gpu.lora_quantize_fp8(t["W"], missing, missing)
+        with pytest.raises(TypeError, match="workspace"):
+            gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, 1.0, 0.1, rng_tensor(0, 0), missing)
+        with pytest.raises(TypeError, match="A must"):
+            gpu.lora_fwd_dropout(t["X"], t["W"], missing, t["B"], Y, 1.0, 0.1, rng_tensor(0, 0), ws)
+    with pytest.raises(gpu.LoraError):
+        gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, 1.0, 0.1, None, ws)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_module_on_an_empty_batch(gpu, fp8):
     m = layer(64, 48, 8, 0.1, fp8)
