@@ -344,8 +344,13 @@ class LoRALinear(torch.nn.Module):
         self.lora_B = torch.nn.Parameter(torch.zeros(d_out, r, **kw))
 
     def quantize_base(self) -> "LoRALinear":
-        """The base weight to 8 bits, in place; returns the layer."""
+        """The base weight to 8 bits, in place; returns the layer.  d_in and
+        d_out have to be multiples of 16 (the codes' rows, and those that dY
+        is rounded to, are read 16 bytes at a time)."""
         if self.weight is not None:
+            if self.d_in % 16 or self.d_out % 16:
+                raise ValueError(f"an 8-bit base needs d_in and d_out as multiples of 16, got {self.d_in} and "
+                                 f"{self.d_out}")
             codes, scales = quantize_weight(self.weight.detach())
             self.weight = None
             self.register_buffer("weight_codes", codes)

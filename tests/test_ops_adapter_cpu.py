@@ -57,6 +57,14 @@ def test_refusals():
             ops.LoRALinear(16, 16, 8, 8.0, dropout=p)
 
 
+@pytest.mark.parametrize("d_in, d_out", [(64, 24), (24, 64)])
+def test_quantize_base_refuses_sizes_that_the_8_bit_layer_does_not_have(d_in, d_out):
+    m = ops.LoRALinear(d_in, d_out, 8, 8.0)
+    with pytest.raises(ValueError, match="multiples of 16"):
+        m.quantize_base()
+    assert m.weight is not None and "weight_codes" not in m.state_dict()
+
+
 @pytest.mark.parametrize("train", [True, False])
 def test_module_traces_without_a_graph_break(train):
     with FakeTensorMode():
