@@ -557,7 +557,7 @@ def _layer_fwd(name, X, base, A, B, Y, scale, p, rng, workspace, stream):
     i = X.get_device()
     args = _pointers(((X, "X", bf16, (M, d_in)), *_base(base, d_out, d_in), (A, "A", bf16, (r, d_in)),
                       (B, "B", bf16, (d_out, r)), (Y, "Y", bf16, (M, d_out))), i)
-    args += (M, d_in, d_out, r, scale, p, _rng_arg(rng, i), *_workspace_arg(workspace, i))
+    args += (M, d_in, d_out, r, float(scale), float(p), _rng_arg(rng, i), *_workspace_arg(workspace, i))
     _call(name, i, args, stream)
 
 
@@ -571,7 +571,7 @@ def _layer_bwd(name, X, base, A, B, dY, dX, dA, dB, scale, p, rng, workspace, fl
     args = _pointers(((X, "X", bf16, (M, d_in)), *_base(base, d_out, d_in), (A, "A", bf16, (r, d_in)),
                       (B, "B", bf16, (d_out, r)), (dY, "dY", bf16, (M, d_out)), (dX, "dX", bf16, (M, d_in)),
                       (dA, "dA", gdt, (r, d_in)), (dB, "dB", gdt, (d_out, r))), i)
-    args += (M, d_in, d_out, r, scale, p, _rng_arg(rng, i), *_workspace_arg(workspace, i), flags)
+    args += (M, d_in, d_out, r, float(scale), float(p), _rng_arg(rng, i), *_workspace_arg(workspace, i), flags)
     _call(name, i, args, stream)
 
 

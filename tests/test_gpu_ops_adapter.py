@@ -287,6 +287,17 @@ def test_missing_tensors_are_named(gpu):
         gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, 1.0, 0.1, None, ws)
 
 
+def test_scale_and_p_may_be_any_number(gpu):
+    t = {k: v.cuda() for k, v in make(8, 64, 64, 8).items()}
+    ws = torch.empty(gpu.lora_bwd_workspace_size(8, 64, 64, 8), dtype=torch.uint8, device="cuda")
+    out = []
+    for scale, p in ((2.0, 0.25), (2, np.float32(0.25)), (np.float32(2.0), torch.tensor(0.25)), (torch.tensor(2.0), 0.25)):
+        Y = torch.empty(8, 64, dtype=BF16, device="cuda")
+        gpu.lora_fwd_dropout(t["X"], t["W"], t["A"], t["B"], Y, scale, p, rng_tensor(3, 4), ws)
+        out.append(Y)
+    assert all(torch.equal(Y, out[0]) for Y in out)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_module_on_an_empty_batch(gpu, fp8):
     m = layer(64, 48, 8, 0.1, fp8)
