@@ -26,7 +26,7 @@ torch._dynamo.explain).  Here:
   backward ops.  W is frozen: it gets no gradient.
 
 * ``torch.ops.lora_b200.lora_linear_adapter(X, W, W_scales, A, B, scale, p,
-  rng)`` is the layer with dropout on the adapter branch (``lora_fwd_dropout``)
+  rng, save)`` is the layer with dropout on the adapter branch (``lora_fwd_dropout``)
   or, with ``W_scales`` (W then holds e4m3 codes), over an 8-bit base
   (``lora_fwd_fp8``), with or without dropout.  It returns (Y, saved), saved
   being T for ``lora_linear_adapter_bwd``.  The mask is drawn from ``rng``, an
@@ -230,10 +230,12 @@ def _check_rng(p: float, rng: Optional[torch.Tensor]):
 
 @torch.library.custom_op(f"{_LIB}::lora_linear_adapter", mutates_args=())
 def lora_linear_adapter(X: torch.Tensor, W: torch.Tensor, W_scales: Optional[torch.Tensor], A: torch.Tensor,
-                        B: torch.Tensor, scale: float, p: float,
-                        rng: Optional[torch.Tensor]) -> Tuple[torch.Tensor, torch.Tensor]:
+                        B: torch.Tensor, scale: float, p: float, rng: Optional[torch.Tensor],
+                        save: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
     """(Y, saved): Y = X W^T + T B^T, T = scale/(1-p) (m * X) A^T, over a bf16
-    base or, with W_scales, over e4m3 codes W."""
+    base or, with W_scales, over e4m3 codes W.  Without ``save`` (no backward
+    will follow) saved is empty and T is not copied out; a backward then
+    computes it again."""
     M, d_in, d_out, r = _check(X, W, A, B)
     _check_rng(p, rng)
     fp8 = W_scales is not None
@@ -248,14 +250,16 @@ def lora_linear_adapter(X: torch.Tensor, W: torch.Tensor, W_scales: Optional[tor
         lora_fwd_fp8(*args, W_scales.contiguous(), *ab, ws, p, rng)
     else:
         lora_fwd_dropout(*args, *ab, p, rng, ws)
+    if not save:
+        return Y, torch.empty(0, dtype=torch.uint8, device=X.device)
     return Y, ws[:max(_saved_bytes(M, r), 1)].clone()
 
 
 @lora_linear_adapter.register_fake
-def _lora_linear_adapter_fake(X, W, W_scales, A, B, scale, p, rng):
+def _lora_linear_adapter_fake(X, W, W_scales, A, B, scale, p, rng, save=True):
     M, d_in, d_out, r = _check(X, W, A, B)
     _check_rng(p, rng)
-    return X.new_empty((M, d_out)), X.new_empty((max(_saved_bytes(M, r), 1),), dtype=torch.uint8)
+    return X.new_empty((M, d_out)), X.new_empty((max(_saved_bytes(M, r), 1) if save else 0,), dtype=torch.uint8)
 
 
 @torch.library.custom_op(f"{_LIB}::lora_linear_adapter_bwd", mutates_args=())
@@ -264,20 +268,23 @@ def lora_linear_adapter_bwd(X: torch.Tensor, W: torch.Tensor, W_scales: Optional
                             rng: Optional[torch.Tensor],
                             fp32_grads: bool = False) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dX, dA, dB) of lora_linear_adapter for the same rng values, with T from
-    ``saved``, which stays as it is (a graph may be gone through twice)."""
+    ``saved``, which stays as it is (a graph may be gone through twice); an
+    empty ``saved`` has T computed again."""
     M, d_in, d_out, r = _check(X, W, A, B)
     gdt = torch.float32 if fp32_grads else A.dtype
     dX = torch.empty((M, d_in), dtype=X.dtype, device=X.device)
     dA = torch.empty((r, d_in), dtype=gdt, device=A.device)
     dB = torch.empty((d_out, r), dtype=gdt, device=B.device)
-    flags = LORA_BWD_T_SAVED | (LORA_BWD_FP32_GRADS if fp32_grads else 0)
+    flags = LORA_BWD_FP32_GRADS if fp32_grads else 0
     args = (X.contiguous(), W.contiguous())
     rest = (A.contiguous(), B.contiguous(), dY.contiguous(), dX, dA, dB, scale)
     fp8 = W_scales is not None
     nbytes = lora_fp8_workspace_size(M, d_in, d_out, r) if fp8 else _workspace_bytes(M, r)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=X.device)
-    t_bytes = _saved_bytes(M, r)
-    ws[:t_bytes].copy_(saved[:t_bytes])
+    if saved.numel() > 0:
+        flags |= LORA_BWD_T_SAVED
+        t_bytes = _saved_bytes(M, r)
+        ws[:t_bytes].copy_(saved[:t_bytes])
     if fp8:
         lora_bwd_fp8(*args, W_scales.contiguous(), *rest, ws, p, rng, flags)
     else:
@@ -291,7 +298,7 @@ def _lora_linear_adapter_bwd_fake(X, W, W_scales, A, B, dY, saved, scale, p, rng
 
 
 def _setup_context_adapter(ctx, inputs, output):
-    X, W, W_scales, A, B, scale, p, rng = inputs
+    X, W, W_scales, A, B, scale, p, rng, _ = inputs
     if W.requires_grad:
         raise RuntimeError("lora_linear: the base weight W is frozen and gets no gradient; "
                            "call W.requires_grad_(False)")
@@ -304,7 +311,8 @@ def _backward_adapter(ctx, dY, _d_saved):
     dX, dA, dB = torch.ops.lora_b200.lora_linear_adapter_bwd(X, W, W_scales, A, B, dY.contiguous(), saved, ctx.scale,
                                                              ctx.p, rng)
     need = ctx.needs_input_grad
-    return (dX if need[0] else None, None, None, dA if need[3] else None, dB if need[4] else None, None, None, None)
+    return (dX if need[0] else None, None, None, dA if need[3] else None, dB if need[4] else None,
+            None, None, None, None)
 
 
 lora_linear_adapter.register_autograd(_backward_adapter, setup_context=_setup_context_adapter)
@@ -365,14 +373,15 @@ class LoRALinear(torch.nn.Module):
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.d_in)
         p = self.dropout if self.training else 0.0
+        # keep T for a backward (it then reads X once less)
+        save = torch.is_grad_enabled() and (x.requires_grad or self.lora_A.requires_grad or self.lora_B.requires_grad)
         if p > 0 or self.weight is None:
             rng = torch.randint(0, 2 ** 62, (2,), dtype=torch.int64, device=x.device) if p > 0 else None
             codes = self.weight is None
             y, _ = torch.ops.lora_b200.lora_linear_adapter(
                 x2, self.weight_codes if codes else self.weight, self.weight_scales if codes else None, self.lora_A,
-                self.lora_B, self.scale, p, rng)
-        elif torch.is_grad_enabled() and (x.requires_grad or self.lora_A.requires_grad or self.lora_B.requires_grad):
-            # keep T for the backward (it then reads X once less)
+                self.lora_B, self.scale, p, rng, save)
+        elif save:
             y, _ = torch.ops.lora_b200.lora_linear_train(x2, self.weight, self.lora_A, self.lora_B, self.scale)
         else:
             y = torch.ops.lora_b200.lora_linear(x2, self.weight, self.lora_A, self.lora_B, self.scale)

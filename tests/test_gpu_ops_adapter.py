@@ -298,6 +298,35 @@ def test_scale_and_p_may_be_any_number(gpu):
     assert all(torch.equal(Y, out[0]) for Y in out)
 
 
+@pytest.mark.parametrize("M", [1, 200])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_forward_that_saves_nothing(gpu, fp8, M):
+    """The same Y, no T; and a backward all the same, from T computed again."""
+    from lora_linear_layer_b200 import ops
+
+    t = {k: v.cuda() for k, v in make(M, 272, 400, 16).items()}
+    W, Ws = ops.quantize_weight(t["W"]) if fp8 else (t["W"], None)
+    rng = rng_tensor(5, 6)
+    results = []
+    for save in (True, False):
+        X, A, B = (t[k].clone().requires_grad_(True) for k in "XAB")
+        Y, saved = torch.ops.lora_b200.lora_linear_adapter(X, W, Ws, A, B, 2.0, 0.25, rng, save)
+        assert (saved.numel() > 0) == save
+        results.append((Y, *torch.autograd.grad(Y, (X, A, B), t["dY"])))
+    for got, want in zip(*results):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_module_saves_only_for_a_backward(gpu, fp8):
+    m = layer(272, 400, 16, 0.0, fp8)
+    x = make(3, 272, 400, 16)["X"].cuda()
+    y = m(x)
+    with torch.no_grad():
+        assert torch.equal(m(x), y.detach())
+    assert y.requires_grad
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_module_on_an_empty_batch(gpu, fp8):
     m = layer(64, 48, 8, 0.1, fp8)

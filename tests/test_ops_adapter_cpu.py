@@ -24,6 +24,7 @@ def test_fake_shapes(fp8):
         Y, saved = torch.ops.lora_b200.lora_linear_adapter(X, W, Ws, A, B, 2.0, 0.1, rng)
         assert Y.shape == (32, 48) and Y.dtype == BF16 and saved.dtype == torch.uint8
         assert saved.numel() == 32 * 16 * 2
+        assert torch.ops.lora_b200.lora_linear_adapter(X, W, Ws, A, B, 2.0, 0.1, rng, False)[1].numel() == 0
         for f32 in (False, True):
             dX, dA, dB = torch.ops.lora_b200.lora_linear_adapter_bwd(X, W, Ws, A, B, Y, saved, 2.0, 0.1, rng, f32)
             assert dX.shape == X.shape and dA.shape == A.shape and dB.shape == B.shape
