@@ -219,8 +219,12 @@ lora_status_t launch_status() {
 // Programmatic dependent launch (PDL) on every launch unless
 // LORA_B200_PDL=0: a kernel's prologue (barrier init, TMEM allocation,
 // descriptor prefetch) then overlaps the tail of the kernel before it on the
-// stream.  Every kernel waits (griddepcontrol.wait) before its first global
-// memory access, so results do not depend on this setting.
+// stream.  Every kernel waits (griddepcontrol.wait) before it reads what the
+// kernel before it writes and before it writes what others may read, so
+// results do not depend on this setting.  (Two begin before they wait, behind a
+// kernel that waits before it lets them go: token_stream_kernel reads weights
+// that were complete earlier, and lowrank_gemm_kernel as dX has inputs that
+// were, and an output that the kernel before it does not touch.)
 bool pdl_enabled() {
   static const bool on = [] {
     const char* e = std::getenv("LORA_B200_PDL");

@@ -31,6 +31,10 @@
 // block before it); the ring has at most seven, so the MMAs that read a buffer
 // are done when the stage that brings its next scales can be filled.
 //
+// dX (late_wait) begins before the kernel in front of it, dA's and dB's, has
+// ended: its inputs were complete when that one began its work.  It waits at
+// its end, so that what follows it still finds everything before it done.
+//
 // Tiles are CTA pairs (cta_group::2) of 256 x BN.  What bounds it is the
 // tensor pipe.
 #pragma once
@@ -48,6 +52,7 @@ constexpr uint32_t kLrScaleBytes = 512u * 3u;  // A: 128 rows, B: 256 columns, 4
 struct LrArgs {
   FusedArgs f;               // sizes, tile counts, stages, ep_bufs
   int32_t group_m;           // M blocks walked together (LrSched)
+  int32_t late_wait;         // the inputs were complete before the kernel before this one began its work
   DropArgs drop;             // DROP: the mask of OUT's [M, N]
 };
 
@@ -165,8 +170,10 @@ __global__ void __launch_bounds__(lr_threads(DROP), 1)
   G::cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_wait();
-  griddep_launch_dependents();
+  if (la.late_wait == 0) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
 
   const int nk = (a.K + kStageK - 1) / kStageK;
   const int nr = (a.r_pad + 63) / 64;  // rank blocks
@@ -448,6 +455,10 @@ __global__ void __launch_bounds__(lr_threads(DROP), 1)
     }
   }
 
+  if (la.late_wait != 0) {  // what follows this kernel may rely on all that came before it
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   tc_fence_before();
   __syncthreads();
   G::cluster_sync();
