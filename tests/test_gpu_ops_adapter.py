@@ -328,6 +328,58 @@ def test_module_saves_only_for_a_backward(gpu, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("M", [5, 200, 1300])
+def test_queued_steps_that_feed_each_other(gpu, fp8, M):
+    """Steps queued one behind another on one workspace, each with a weight
+    that was written just before it and the dX of the step before as its dY:
+    the results of the same steps with a wait after every call, bit for bit."""
+    L, d, r, steps = gpu, 768, 16, 12
+    g = torch.Generator().manual_seed(3)
+    rand = lambda *shape: (torch.randn(*shape, generator=g) * shape[-1] ** -0.5).to(BF16).cuda()
+    weights, inputs = [rand(d, d) for _ in range(steps)], [rand(M, d) * 20 for _ in range(steps)]
+    A, B, first = rand(r, d), rand(d, r), rand(M, d) * 20
+    size = (L.lora_fp8_workspace_size if fp8 else L.lora_bwd_workspace_size)(M, d, d, r)
+    rng = rng_tensor(11, 12)
+
+    def run(wait):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        W = torch.zeros(d, d, dtype=BF16, device="cuda")
+        Wq = torch.zeros(d, d, dtype=torch.float8_e4m3fn, device="cuda")
+        Ws = torch.zeros(d // 128, d // 128, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+        out = [{n: torch.empty(*shape, dtype=BF16, device="cuda")
+                for n, shape in (("Y", (M, d)), ("dX", (M, d)), ("dA", (r, d)), ("dB", (d, r)))} for _ in range(steps)]
+        dY = first
+        torch.cuda.synchronize()
+        for X, new, o in zip(inputs, weights, out):
+            calls = []
+            if fp8:
+                calls.append(lambda: L.lora_quantize_fp8(new, Wq, Ws))
+                calls.append(lambda: L.lora_fwd_fp8(X, Wq, Ws, A, B, o["Y"], 2.0, ws, 0.25, rng))
+                calls.append(lambda: L.lora_bwd_fp8(X, Wq, Ws, A, B, dY, o["dX"], o["dA"], o["dB"], 2.0, ws, 0.25, rng,
+                                                    L.LORA_BWD_T_SAVED))
+            else:
+                calls.append(lambda: L.lora_restore(new, W))
+                calls.append(lambda: L.lora_fwd_dropout(X, W, A, B, o["Y"], 2.0, 0.25, rng, ws))
+                calls.append(lambda: L.lora_bwd_dropout(X, W, A, B, dY, o["dX"], o["dA"], o["dB"], 2.0, 0.25, rng, ws,
+                                                        L.LORA_BWD_T_SAVED))
+            for call in calls:
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            dY = o["dX"]
+        torch.cuda.synchronize()
+        return out
+
+    want = run(True)
+    assert all(torch.isfinite(t.float()).all() for o in want for t in o.values())
+    for _ in range(10):
+        for o, w in zip(run(False), want):
+            for n in w:
+                assert torch.equal(o[n], w[n]), n
+    assert L.lora_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_module_on_an_empty_batch(gpu, fp8):
     m = layer(64, 48, 8, 0.1, fp8)
     x = torch.empty(2, 0, 64, dtype=BF16, device="cuda", requires_grad=True)
