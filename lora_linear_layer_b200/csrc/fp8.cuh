@@ -156,8 +156,8 @@ constexpr int kQuantThreads = 256;
 // ceil(cols/128)] bytes.  cols is a multiple of 16.  Grid: one block for each
 // 128 x 128 block of W, columns fastest.
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_block_kernel(const uint8_t* __restrict__ W, uint8_t* __restrict__ Wq, uint8_t* __restrict__ Ws,
-                          int32_t rows, int32_t cols, int32_t col_blocks) {
+    quantize_block_kernel(const uint8_t* W, uint8_t* Wq, uint8_t* Ws, int32_t rows, int32_t cols,
+                          int32_t col_blocks) {
   __shared__ uint32_t warp_max[kQuantThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
@@ -168,11 +168,14 @@ __global__ void __launch_bounds__(kQuantThreads)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + 32 * i;
-    const bool in = row < rows && col < cols;
-    const uint4* src = reinterpret_cast<const uint4*>(W + (size_t(row) * size_t(cols) + size_t(col)) * 2);
-    v[i][0] = in ? __ldcs(src) : make_uint4(0, 0, 0, 0);
-    v[i][1] = in ? __ldcs(src + 1) : make_uint4(0, 0, 0, 0);
+    // (what is not there repeats the last values; every load is unconditional)
+    const uint8_t* src = W + (size_t(imin(row, rows - 1)) * size_t(cols) + size_t(imin(col, cols - 16))) * 2;
+    v[i][0] = ld_global_cs_v4(src);
+    v[i][1] = ld_global_cs_v4(src + 16);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (row0 + 32 * i >= rows || col >= cols) v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
   uint32_t m = amax_bf16x16(v[0][0], v[0][1]);
 #pragma unroll
   for (int i = 1; i < 4; ++i) m = amax_bf16x2(m, amax_bf16x16(v[i][0], v[i][1]));
@@ -200,20 +203,20 @@ __global__ void __launch_bounds__(kQuantThreads)
 // in two halves of each 32-byte sector, took 38 us instead of 23 on 14336 x
 // 4096).
 __global__ void __launch_bounds__(kQuantThreads)
-    dequantize_block_kernel(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Ws, uint8_t* __restrict__ W,
-                            int32_t rows, int32_t cols, int32_t col_blocks) {
+    dequantize_block_kernel(const uint8_t* Wq, const uint8_t* Ws, uint8_t* W, int32_t rows, int32_t cols,
+                            int32_t col_blocks) {
   griddep_wait();
   griddep_launch_dependents();
   const int cb = int(blockIdx.x) % col_blocks, rb = int(blockIdx.x) / col_blocks;
   const int col = cb * kQBlock + int(threadIdx.x & 15u) * 8;
   const int row0 = rb * kQBlock + int(threadIdx.x >> 4);
   if (col >= cols) return;
-  const float s = e8m0_value(Ws[blockIdx.x]);
+  const float s = e8m0_value(ld_global_u8(Ws + blockIdx.x));
   uint2 q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = imin(row0 + 16 * i, rows - 1);
-    q[i] = __ldcs(reinterpret_cast<const uint2*>(Wq + size_t(row) * size_t(cols) + size_t(col)));
+    q[i] = ld_global_cs_v2(Wq + size_t(row) * size_t(cols) + size_t(col));
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPrepThreads) token_prep_kernel(const PrepArgs
       const int k = k0 + u * kStep + t * 8;
       const size_t at = size_t(imin(k, a.K - 8)) * 2;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[u][i] = __ldg(reinterpret_cast<const uint4*>(src[i] + at));
+      for (int i = 0; i < 4; ++i) v[u][i] = ld_global_v4(src[i] + at);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
