@@ -256,23 +256,33 @@ __global__ void __launch_bounds__(kMergeThreads, 1) merge_kernel(const __grid_co
 // The plain copy and fill kernels have internal linkage: this header is
 // included by more than one translation unit of the library.
 
-// W_dst <- W_src, 16 bytes per thread per step (restore from pristine).
-static __global__ void copy16_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, size_t n16) {
+// W_dst <- W_src, 16 bytes per thread per step (restore from pristine), four
+// steps' loads in flight.  (The loads are the coherent ones of ptx.cuh: the
+// kernel before this one may be what writes W_src.)
+static __global__ void copy16_kernel(const uint4* src, uint4* dst, size_t n16) {
   griddep_launch_dependents();
   griddep_wait();
-  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x)
-    dst[i] = src[i];
+  const size_t step = (size_t)gridDim.x * blockDim.x;
+  size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
+  for (; i + 3 * step < n16; i += 4 * step) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = ld_global_v4(src + i + u * step);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) dst[i + u * step] = v[u];
+  }
+  for (; i < n16; i += step) dst[i] = ld_global_v4(src + i);
 }
 
 // Tail of a copy that is not a multiple of 16 bytes (2-byte elements).
-static __global__ void copy2_kernel(const uint16_t* __restrict__ src, uint16_t* __restrict__ dst, size_t n) {
+static __global__ void copy2_kernel(const uint16_t* src, uint16_t* dst, size_t n) {
   griddep_launch_dependents();
   griddep_wait();
   const size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
   if (i < n) dst[i] = src[i];
 }
 
-static __global__ void zero16_kernel(uint4* __restrict__ dst, size_t n16) {
+static __global__ void zero16_kernel(uint4* dst, size_t n16) {
   griddep_launch_dependents();
   griddep_wait();
   for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x)

@@ -9,7 +9,7 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "lora_linear_layer_b200", "csrc")
-FILES = ("adapter_api.cuh", "adapter_pass.cuh", "fp8.cuh", "lowrank_gemm.cuh", "philox.cuh", "token.cuh")
+FILES = sorted(n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh")))
 
 
 def code(name):
