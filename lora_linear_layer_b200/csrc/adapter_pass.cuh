@@ -13,13 +13,14 @@
 // order (no atomics: results repeat bit for bit).
 //
 // What bounds it is the read of P (and the write of its codes).  So P comes
-// by TMA as in the plain product, several stages ahead, and eight warps work
-// on each stage in shared memory between the copy and the MMA: they take the
-// maximum of a row's 128 values over 4 lanes, write the codes to global
-// memory, and put the masked values back where the MMA reads them (a dropped
-// value is set to zero by a select, so the product needs no mask and a
-// dropped infinity or NaN is gone; 1/(1-p) is in the scale).  The mask is
-// computed here, 8 values at a time, for the chunk in hand.
+// by TMA as in the plain product, several stages ahead, and 8 or 16 warps
+// (pass_workers) work on each stage in shared memory between the copy and
+// the MMA: they take the maximum of a row's 128 values over 4 lanes, write
+// the codes to global memory, and put the masked values back where the MMA
+// reads them (a dropped value is set to zero by a select, so the product
+// needs no mask and a dropped infinity or NaN is gone; 1/(1-p) is in the
+// scale).  The mask is computed here, 8 values at a time, for the chunk in
+// hand.
 #pragma once
 
 #include "common.cuh"
@@ -395,10 +396,19 @@ __global__ void __launch_bounds__(pass_threads(RCW, P_MN, QUANT), pass_workers(R
       if (g >= a.rows) continue;
       const float v[4] = {acc.x * a.scale, acc.y * a.scale, acc.z * a.scale, acc.w * a.scale};
       if (a.out_mode == OUT_ROWS_RPAD) {
+        // T and dT go to bf16 because they are the operands of the next
+        // product, whose other side is bf16 (kind::f16 takes one type for
+        // both).  Columns past the rank are zero and not the sum: a row with
+        // an infinity has NaN there (infinity times zero fill), which the
+        // next product would spread over its whole row.
+        if (j0 >= a.r) {  // r % 8 == 0: the 4 columns are all in or all out
+          *reinterpret_cast<uint2*>(a.out + size_t(g) * size_t(a.r_pad) + j0) = make_uint2(0u, 0u);
+          continue;
+        }
         *reinterpret_cast<uint2*>(a.out + size_t(g) * size_t(a.r_pad) + j0) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       } else if (a.out_mode == OUT_ROWS_R) {
-        if (j0 >= a.r) continue;  // r % 8 == 0: the 4 columns are all in or all out
+        if (j0 >= a.r) continue;
         const size_t o = size_t(g) * size_t(a.r) + j0;
         if (a.out_f32)
           *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + o) = make_float4(v[0], v[1], v[2], v[3]);

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kPrepThreads) token_prep_kernel(const PrepArgs
     float s = 0.0f;
 #pragma unroll
     for (uint32_t c = 0; c < uint32_t(kPrepSplits); ++c) s += ld_shared_cluster_f32(mapa_shared(smem_addr(sums + i), c));
-    if (m0 + tok < a.M)
+    if (m0 + tok < a.M)  // (bf16, and zero past the rank, as adapter_pass_kernel leaves it)
       a.T[size_t(m0 + tok) * size_t(a.r_pad) + size_t(j0 + j)] =
           __float2bfloat16_rn(j0 + j < a.r ? s * a.scale : 0.0f);
   }
