@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(pass_threads(RCW, P_MN, QUANT), pass_workers(R
   constexpr int kPassWorkers = pass_workers(RCW, P_MN, QUANT), kPassThreads = pass_threads(RCW, P_MN, QUANT);
   if constexpr (QUANT) {
     if (int(blockIdx.x) >= x_atoms) {  // blocks behind the row tiles: the other operand's scales
-      griddep_wait();
+      griddep_wait();  // must come first, as below
       griddep_launch_dependents();
       const int blocks = int(gridDim.x) - x_atoms, block = int(blockIdx.x) - x_atoms + blocks * int(blockIdx.y);
       scale_atoms(atoms, block * (kPassThreads / 32) + int(threadIdx.x >> 5),
@@ -145,8 +145,10 @@ __global__ void __launch_bounds__(pass_threads(RCW, P_MN, QUANT), pass_workers(R
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The wait comes first: a kernel launched behind this one may then read
-  // what was finished before this one began (its weights), beside it.
+  // The wait must come first, in every block: token_stream_kernel and
+  // lowrank_gemm_kernel (late_wait) behind this one read, before their own
+  // wait, what was written before this one.  That is complete only if this
+  // one lets them go after it has waited itself.
   griddep_wait();
   griddep_launch_dependents();
 

@@ -32,8 +32,10 @@
 // are done when the stage that brings its next scales can be filled.
 //
 // dX (late_wait) begins before the kernel in front of it, dA's and dB's, has
-// ended: its inputs were complete when that one began its work.  It waits at
-// its end, so that what follows it still finds everything before it done.
+// ended: its inputs were complete when that one began its work, since that one
+// waits before it lets a dependent launch go (adapter_pass_kernel must).  It
+// waits at its end, so that what follows it still finds everything before it
+// done.
 //
 // Tiles are CTA pairs (cta_group::2) of 256 x BN.  What bounds it is the
 // tensor pipe.

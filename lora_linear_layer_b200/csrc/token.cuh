@@ -61,6 +61,8 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 __global__ void __launch_bounds__(kPrepThreads) token_prep_kernel(const PrepArgs a) {
   __shared__ float part[kPrepWarps][kPrepTokens][kPrepRanks + 1];
   __shared__ __align__(16) float sums[kPrepTokens * kPrepRanks];
+  // The wait must come first, in every block: token_stream_kernel behind this
+  // one reads the weight before its own wait (see adapter_pass_kernel).
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -22,3 +22,14 @@ def code(name):
 def test_no_load_that_may_pass_the_wait(name):
     found = re.findall(r"__ldg\b|__ldc[agsv]\b|__ldlu\b|ld\.global\.nc|__restrict__", code(name))
     assert not found, (name, found)
+
+
+@pytest.mark.parametrize("name,kernel", [("adapter_pass.cuh", "adapter_pass_kernel"), ("token.cuh", "token_prep_kernel")])
+def test_kernels_in_front_of_an_early_reader_wait_before_they_let_it_go(name, kernel):
+    """token_stream_kernel and dX's lowrank_gemm_kernel read before their own
+    wait what was written before the kernel in front of them: that kernel
+    calls griddep_wait directly before every griddep_launch_dependents."""
+    body = code(name).split(kernel + "(", 1)[1].split("__global__", 1)[0]
+    calls = re.findall(r"griddep_\w+\(\);", body)
+    assert calls and calls == ["griddep_wait();", "griddep_launch_dependents();"] * (len(calls) // 2)
+    assert len(re.findall(r"griddep_wait\(\);\s*griddep_launch_dependents\(\);", body)) == len(calls) // 2
