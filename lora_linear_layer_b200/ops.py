@@ -334,7 +334,8 @@ class LoRALinear(torch.nn.Module):
     ``quantize_base()`` turns the base weight into 8 bits (e4m3 codes, one
     power-of-two scale for each 128 x 128 block), as buffers ``weight_codes``
     and ``weight_scales`` in place of ``weight``: half the memory, and 8-bit
-    products in forward and backward."""
+    products in forward and backward.  A cast of the module (``.to(dtype)``,
+    ``.half()``) leaves these two as they are."""
 
     def __init__(self, d_in: int, d_out: int, r: int, alpha: float, rslora: bool = False,
                  device: Optional[torch.device] = None, generator: Optional[torch.Generator] = None,
@@ -364,6 +365,18 @@ class LoRALinear(torch.nn.Module):
             self.register_buffer("weight_codes", codes)
             self.register_buffer("weight_scales", scales)
         return self
+
+    def _apply(self, fn, recurse=True):
+        # codes and scales are bytes, not numbers of a precision: casts pass
+        # them by (as uint8), moves take them along
+        def keep(t):
+            if t.dtype not in (torch.float8_e4m3fn, torch.float8_e8m0fnu):
+                return fn(t)
+            held = t.view(torch.uint8)
+            moved = fn(held)
+            return (moved if moved.dtype == torch.uint8 else held.to(moved.device)).view(t.dtype)
+
+        return super()._apply(keep, recurse)
 
     def base_weight(self) -> torch.Tensor:
         """The base weight's values in bf16."""
