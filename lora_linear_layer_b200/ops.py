@@ -199,12 +199,16 @@ lora_linear.register_autograd(_backward, setup_context=_setup_context)
 
 # ------------------------------------- dropout and the 8-bit base ----
 
+def _empty_codes(d_out: int, d_in: int, device) -> Tuple[torch.Tensor, torch.Tensor]:
+    return (torch.empty((d_out, d_in), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty(((d_out + 127) // 128, (d_in + 127) // 128), dtype=torch.float8_e8m0fnu, device=device))
+
+
 def quantize_weight(W: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """(codes float8_e4m3fn [d_out, d_in], scales float8_e8m0fnu, one power of
     two for each 128 x 128 block) of a bf16 weight (``lora_quantize_fp8``)."""
     d_out, d_in = W.shape
-    codes = torch.empty((d_out, d_in), dtype=torch.float8_e4m3fn, device=W.device)
-    scales = torch.empty(((d_out + 127) // 128, (d_in + 127) // 128), dtype=torch.float8_e8m0fnu, device=W.device)
+    codes, scales = _empty_codes(d_out, d_in, W.device)
     lora_quantize_fp8(W.contiguous(), codes, scales)
     return codes, scales
 
@@ -335,7 +339,8 @@ class LoRALinear(torch.nn.Module):
     power-of-two scale for each 128 x 128 block), as buffers ``weight_codes``
     and ``weight_scales`` in place of ``weight``: half the memory, and 8-bit
     products in forward and backward.  A cast of the module (``.to(dtype)``,
-    ``.half()``) leaves these two as they are."""
+    ``.half()``) leaves these two as they are, and a checkpoint that has them
+    turns a layer with a bf16 base into the 8-bit form as it loads."""
 
     def __init__(self, d_in: int, d_out: int, r: int, alpha: float, rslora: bool = False,
                  device: Optional[torch.device] = None, generator: Optional[torch.Generator] = None,
@@ -360,11 +365,21 @@ class LoRALinear(torch.nn.Module):
             if self.d_in % 16 or self.d_out % 16:
                 raise ValueError(f"an 8-bit base needs d_in and d_out as multiples of 16, got {self.d_in} and "
                                  f"{self.d_out}")
-            codes, scales = quantize_weight(self.weight.detach())
-            self.weight = None
-            self.register_buffer("weight_codes", codes)
-            self.register_buffer("weight_scales", scales)
+            self._hold_codes(*quantize_weight(self.weight.detach()))
         return self
+
+    def _hold_codes(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.weight = None
+        self.register_buffer("weight_codes", codes)
+        self.register_buffer("weight_scales", scales)
+
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        given = [state_dict.get(prefix + name) for name in ("weight_codes", "weight_scales")]
+        if self.weight is not None and all(g is not None for g in given):
+            room = _empty_codes(self.d_out, self.d_in, self.weight.device)
+            if all(g.shape == e.shape for g, e in zip(given, room)):  # (other sizes are refused below)
+                self._hold_codes(*room)
+        super()._load_from_state_dict(state_dict, prefix, *args)
 
     def _apply(self, fn, recurse=True):
         # codes and scales are bytes, not numbers of a precision: casts pass

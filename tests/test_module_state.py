@@ -68,3 +68,65 @@ def test_codes_move_to_another_device():
     m = m.to_empty(device="cpu")
     assert m.weight_codes.device.type == "cpu" and m.weight_codes.shape == (272, 160)
     raw(m)
+
+
+def plain_layer(seed=1):
+    return ops.LoRALinear(160, 272, 8, 16.0, generator=torch.Generator().manual_seed(seed))
+
+
+@pytest.mark.parametrize("assign", [False, True])
+@pytest.mark.parametrize("through_file", [False, True])
+def test_a_checkpoint_of_a_quantised_layer_loads_into_a_fresh_one(assign, through_file):
+    """Into a layer with a bf16 base and into one in the 8-bit form, alone and
+    inside a model."""
+    src = quantized_layer(seed=3)
+    state = {"0." + k: v for k, v in src.state_dict().items()}
+    assert sorted(state) == ["0.lora_A", "0.lora_B", "0.weight_codes", "0.weight_scales"]
+    if through_file:
+        f = io.BytesIO()
+        torch.save(state, f)
+        f.seek(0)
+        state = torch.load(f, weights_only=True)
+    for fresh in (plain_layer(), quantized_layer(seed=4)):
+        model = torch.nn.Sequential(fresh)
+        result = model.load_state_dict(state, strict=True, assign=assign)
+        assert not result.missing_keys and not result.unexpected_keys
+        m = model[0]
+        assert m.weight is None and "base=e4m3" in repr(m)
+        for a, b in zip(raw(m), raw(src)):
+            assert torch.equal(a, b)
+        assert torch.equal(m.lora_A, src.lora_A) and torch.equal(m.lora_B, src.lora_B)
+        assert sorted(m.state_dict()) == sorted(src.state_dict())
+        if not assign:
+            assert m.weight_codes.data_ptr() != state["0.weight_codes"].data_ptr()
+
+
+def test_a_checkpoint_fills_a_layer_built_on_meta():
+    src = quantized_layer(seed=5)
+    m = ops.LoRALinear(160, 272, 8, 16.0, device="meta")
+    m.load_state_dict(src.state_dict(), assign=True)
+    for a, b in zip(raw(m), raw(src)):
+        assert torch.equal(a, b)
+
+
+def test_other_checkpoints_are_refused_and_leave_the_weight():
+    """Codes of another layer's size, codes without scales, and a bf16
+    checkpoint for an 8-bit layer."""
+    m = plain_layer()
+    for state in (quantized_layer(d_in=176).state_dict(), quantized_layer(d_out=16).state_dict(),
+                  {k: v for k, v in quantized_layer().state_dict().items() if k != "weight_scales"}):
+        with pytest.raises(RuntimeError, match="weight"):
+            m.load_state_dict(state)
+        assert m.weight is not None and torch.equal(m.weight, plain_layer().weight)
+    q = quantized_layer()
+    before = [b.clone() for b in raw(q)]
+    with pytest.raises(RuntimeError, match="weight_codes"):
+        q.load_state_dict(m.state_dict())
+    for a, b in zip(raw(q), before):
+        assert torch.equal(a, b)
+
+
+def test_plain_checkpoints_load_as_before():
+    src, m = plain_layer(2), plain_layer(3)
+    m.load_state_dict(src.state_dict())
+    assert torch.equal(m.weight, src.weight) and sorted(m.state_dict()) == ["lora_A", "lora_B", "weight"]
