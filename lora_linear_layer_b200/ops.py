@@ -342,6 +342,8 @@ class LoRALinear(torch.nn.Module):
     ``.half()``) leaves these two as they are, and a checkpoint that has them
     turns a layer with a bf16 base into the 8-bit form as it loads."""
 
+    dropout = 0.0  # (of a layer that was pickled before it had one)
+
     def __init__(self, d_in: int, d_out: int, r: int, alpha: float, rslora: bool = False,
                  device: Optional[torch.device] = None, generator: Optional[torch.Generator] = None,
                  dropout: float = 0.0):

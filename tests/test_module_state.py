@@ -130,3 +130,18 @@ def test_plain_checkpoints_load_as_before():
     src, m = plain_layer(2), plain_layer(3)
     m.load_state_dict(src.state_dict())
     assert torch.equal(m.weight, src.weight) and sorted(m.state_dict()) == ["lora_A", "lora_B", "weight"]
+
+
+def test_a_layer_pickled_without_dropout_still_runs():
+    """Layers pickled whole before the module had a dropout have no such
+    attribute."""
+    m = plain_layer()
+    assert m.__dict__.pop("dropout") == 0.0
+    f = io.BytesIO()
+    torch.save(m, f)
+    f.seek(0)
+    m = torch.load(f, weights_only=False)
+    with torch._subclasses.fake_tensor.FakeTensorMode(allow_non_fake_inputs=True):
+        x = torch.empty(3, 160, dtype=torch.bfloat16)
+        assert m(x).shape == (3, 272) and m.eval()(x).shape == (3, 272)
+    assert "dropout" not in repr(m)
