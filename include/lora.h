@@ -79,7 +79,7 @@ typedef enum {
   LORA_ERR_UNSUPPORTED_DEVICE = 8, /* current device is not sm_100 */
   LORA_ERR_ALIAS = 9,              /* an output overlaps an input */
   LORA_ERR_FLAGS = 10,             /* a flags argument has an unknown bit set */
-  LORA_ERR_DROPOUT = 11            /* p outside [0, 1), or p > 0 without a seed and offset */
+  LORA_ERR_DROPOUT = 11            /* p outside [0, 1), or t = 65536 (below), or p > 0 without a seed and offset */
 } lora_status_t;
 
 /* ABI version of the loaded library (LORA_ABI_VERSION it was built with). */
@@ -349,7 +349,8 @@ lora_status_t lora_restore(const void* W_src, void* W_dst, int64_t n_elems, void
  * (Philox4x32 with 7 rounds): X's element (i, k) is kept when lane k % 8 of
  * the 8 16-bit lanes (low half of word 0 first) of the block with counter
  * (k / 8, i, offset low word, offset high word) and key (seed low, seed
- * high) is at least t = round(65536 p); 1-p stands for 1 - t/65536.  A
+ * high) is at least t = round(65536 p); 1-p stands for 1 - t/65536, and a p
+ * with t = 65536 (from 1 - 2^-17 on) is refused with LORA_ERR_DROPOUT.  A
  * dropped value counts as zero even if it is infinite or NaN.
  *   `rng`: DEVICE memory, 16-byte aligned, two uint64: seed and offset, read
  *   when the kernels run.  A captured graph therefore draws a new mask at

@@ -153,7 +153,7 @@ const char* lora_status_string(lora_status_t s) {
     case LORA_ERR_UNSUPPORTED_DEVICE: return "LORA_ERR_UNSUPPORTED_DEVICE: needs an sm_100 (B200) device";
     case LORA_ERR_ALIAS: return "LORA_ERR_ALIAS: an output overlaps an input";
     case LORA_ERR_FLAGS: return "LORA_ERR_FLAGS: unknown bit in a flags argument";
-    case LORA_ERR_DROPOUT: return "LORA_ERR_DROPOUT: p outside [0, 1) or no seed and offset for p > 0";
+    case LORA_ERR_DROPOUT: return "LORA_ERR_DROPOUT: p outside [0, 1), or 1 as a multiple of 1/65536, or no seed and offset for p > 0";
   }
   return "LORA_ERR_UNKNOWN";
 }

@@ -45,6 +45,7 @@ Argument marshalling only: all arithmetic runs in the library's kernels.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from typing import Optional, Tuple
 
@@ -349,8 +350,9 @@ class LoRALinear(torch.nn.Module):
                  dropout: float = 0.0):
         super().__init__()
         self.d_in, self.d_out, self.r, self.alpha = int(d_in), int(d_out), int(r), float(alpha)
-        if not 0.0 <= dropout < 1.0:
-            raise ValueError(f"dropout must be in [0, 1), got {dropout}")
+        # (as the library holds it: fp32, then a multiple of 1/65536)
+        if not 0.0 <= ctypes.c_float(dropout).value < 1.0 - 2.0 ** -17:
+            raise ValueError(f"dropout must be in [0, 1), and below 1 as a multiple of 1/65536, got {dropout}")
         self.dropout = float(dropout)
         self.scale = self.alpha / (math.sqrt(self.r) if rslora else self.r)
         kw = dict(dtype=torch.bfloat16, device=device)

@@ -145,3 +145,19 @@ def test_a_layer_pickled_without_dropout_still_runs():
         x = torch.empty(3, 160, dtype=torch.bfloat16)
         assert m(x).shape == (3, 272) and m.eval()(x).shape == (3, 272)
     assert "dropout" not in repr(m)
+
+
+def test_dropout_that_would_drop_everything_is_refused_at_once():
+    """p is held as round(65536 p) / 65536: from 1 - 2^-17 on that is 1, which
+    the library refuses at every call."""
+    for p in (1.0 - 2.0 ** -17, 0.999999, 1.0 - 2.0 ** -30, 1.0):
+        with pytest.raises(ValueError, match="dropout"):
+            ops.LoRALinear(16, 16, 8, 8.0, dropout=p)
+    for p in (0.0, 1e-9, 1.0 - 2.0 ** -16, 1.0 - 2.0 ** -17 - 2.0 ** -23):
+        assert ops.LoRALinear(16, 16, 8, 8.0, dropout=p).dropout == p
+    with torch.device("meta"):
+        assert ops.LoRALinear(16, 16, 8, 8.0, dropout=0.1).lora_A.is_meta
+
+
+def test_the_refusal_of_p_names_the_rounding(built_lib):
+    assert "65536" in built_lib.lora_status_string(11)
