@@ -69,9 +69,18 @@ struct PassCfg {
 };
 
 // Three stages where two blocks share an SM (37 KB each at r = 16), else as
-// many as fit, at most six; the splits of a row tile form one cluster, as many
-// as fill the resident block slots, at most 8 and at least 256 values of the
-// contraction each.
+// many as fit, at most six.  The splits of a row tile form one cluster: as many
+// as fill the block slots that shared memory and threads leave, at most 8 and
+// at least 256 values of the contraction each.
+// For dA and dB (66 registers, 320 threads) these are more slots than there
+// are: shared memory has room for 3 or 4 blocks, the registers for 2.  The
+// blocks past the resident ones even out the masked row tiles of dA and the
+// cheaper ones of dB.  With the slots held to 2 an SM the launch takes 290-320
+// us against 230-240 on 16384 x 4096 x 14336, r = 64, p = 0.1, and 67 against
+// 58-63 on 8192 x 4096 x 4096, r = 16; less only where a few row tiles remain
+// (2400 x 4096 x 4096, r = 32, no mask: 24 against 30).  (The occupancy query
+// does not say how many are resident: for a kernel that allocates tensor memory
+// it answers one block an SM, where two and three were seen to run.)
 void pick_pass(int64_t rows, int64_t K, int r, bool p_mn, bool r_mn, bool quant, int out_mode, int64_t launch_tiles,
                int sm_count, PassCfg& c) {
   const int r_pad = r_pad_of(r);
@@ -88,8 +97,10 @@ void pick_pass(int64_t rows, int64_t K, int r, bool p_mn, bool r_mn, bool quant,
   const int block_k = p_mn ? 64 : 128;
   const int nb = int((K + block_k - 1) / block_k);
   const int tiles = int(std::max<int64_t>(1, launch_tiles));
-  // (one block an SM: two clusters of 8 fit a GPC, so that 17 row tiles took
-  // two rounds, 28 us on X[2051, 2560] at r = 128 against 17 us in fours)
+  // One block an SM: two clusters of 8 fit most GPCs, 15 the chip (and 15 of 7,
+  // 22 of 6, 33 of 4), so that 17 row tiles took two rounds, 28 us on
+  // X[2051, 2560] at r = 128 against 15-17 us in fours; sixes are no faster
+  // (14.5, and dT 22 in either).
   const int most = per_sm == 1 && tiles > 14 ? 4 : 8;
   int splits = std::max(1, std::min({per_sm * sm_count / tiles, most, std::max(1, nb * block_k / 256)}));
   a.nb_per_split = std::max(1, (nb + splits - 1) / splits);
@@ -362,7 +373,8 @@ lora_status_t launch_stream_t(const CUtensorMap* maps, const StreamArgs& a, int 
 // side).  Above 128 tokens its blocks' way out, 128 rows by every token, costs
 // as much as a short contraction (X[223, 288], N = 1664 at 8 bits: 21 us
 // against 9 us by tiles; [256, 4096], N = 4096: 22 against 17 us), and it
-// pays for splitting a long one alone ([256, 14336], N = 4096: 32 against 74).
+// pays for splitting a long one alone ([256, 14336], N = 4096: 32 against 74);
+// K = 6144 lies between these two.
 bool use_stream(int64_t M, int64_t K, bool drop) {
   return M <= 128 || (M <= (drop ? kStreamMaxDrop : kStreamMax) && K > 6144);
 }
