@@ -256,22 +256,14 @@ __global__ void __launch_bounds__(kMergeThreads, 1) merge_kernel(const __grid_co
 // The plain copy and fill kernels have internal linkage: this header is
 // included by more than one translation unit of the library.
 
-// W_dst <- W_src, 16 bytes per thread per step (restore from pristine), four
-// steps' loads in flight.  (The loads are the coherent ones of ptx.cuh: the
-// kernel before this one may be what writes W_src.)
+// W_dst <- W_src, 16 bytes per thread per step (restore from pristine).  The
+// load is the coherent one of ptx.cuh: the kernel before this one may be what
+// writes W_src.  (Four steps unrolled: 42 against 40.2 us on 14336 x 4096.)
 static __global__ void copy16_kernel(const uint4* src, uint4* dst, size_t n16) {
   griddep_launch_dependents();
   griddep_wait();
-  const size_t step = (size_t)gridDim.x * blockDim.x;
-  size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
-  for (; i + 3 * step < n16; i += 4 * step) {
-    uint4 v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = ld_global_v4(src + i + u * step);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) dst[i + u * step] = v[u];
-  }
-  for (; i < n16; i += step) dst[i] = ld_global_v4(src + i);
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x)
+    dst[i] = ld_global_v4(src + i);
 }
 
 // Tail of a copy that is not a multiple of 16 bytes (2-byte elements).
